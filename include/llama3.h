@@ -352,6 +352,168 @@ int llama3_generation_advance(int32_t* positions, int32_t* ids, int32_t* history
                               int32_t* done, int eos_id, int batch, int history_rows,
                               long long history_stride, llama3_stream_t stream);
 
+/* ---- drafted trees: verifying several drafted tokens in one step ----
+ *
+ * A drafter proposes a tree of tokens per sequence; the model runs over all of
+ * its nodes at once and keeps the longest path its own choices confirm
+ * (speculative decoding with a token tree; no counterpart on the pages).
+ * The tree: parents is device int32 [batch, n_nodes]; parents[b][t] is the
+ * node that node t continues, or -1 for a node that continues the cached
+ * sequence itself.  A node comes behind its parent (parents[b][t] < t).  A
+ * value below -1 marks padding: the node, and every node below it, takes no
+ * part (sequences of one batch may so have trees of different sizes).
+ * parents[b][t] >= t is reported as LLAMA3_ERR_ARG through
+ * llama3_device_status, and the node counts as padding.
+ * The keys and values of the nodes live in buffers of their own, [batch,
+ * n_nodes, KV, hd] per layer, until a path of them is committed: a rejected
+ * node never enters the cache.  n_nodes <= LLAMA3_MAX_TREE_NODES.
+ */
+#define LLAMA3_MAX_TREE_NODES 256
+
+/* Bytes of workspace that llama3_attention_tree needs (0 is possible). */
+int llama3_tree_workspace_size(const llama3_config* cfg, int batch, int n_nodes, int max_len, size_t* bytes);
+
+/*
+ * Attention of a drafted tree over a cache: for node t of sequence b and query
+ * head h (KV head g = h / (H/KV)),
+ *   out[b, t, h] = softmax_j(q[b,t,h] . k_j / sqrt(hd)) v_j
+ * over the cached rows j = 0 .. kv_lens[b]-1 of (b, g) and, of the tree, the
+ * node itself and its ancestors.  Other nodes and the cache behind kv_lens[b]
+ * have no influence, whatever they hold (infinities and NaN included).
+ * q: [batch, n_nodes, H, hd] and k_nodes, v_nodes: [batch, n_nodes, KV, hd],
+ * rotated to the node's position (the cached length plus its depth, where
+ * nothing was evicted); caches as in llama3_layer_forward; kv_lens: device
+ * int32 [batch], in [0, max_len] (a value outside is clamped and reported as
+ * LLAMA3_ERR_ARG through llama3_device_status), max_len <= cache_cap being a
+ * bound the caller knows without reading it.  out: [batch, n_nodes, H*hd];
+ * rows of padding nodes are written as zeros.
+ * ws: at least llama3_tree_workspace_size(cfg, batch, n_nodes, max_len) bytes.
+ * Errors: LLAMA3_ERR_ARG (null pointers, n_nodes outside [1, 256], max_len
+ * outside [0, cache_cap], ...), LLAMA3_ERR_ALIGN (kv_lens and parents 4-byte,
+ * all others 16-byte aligned), LLAMA3_ERR_WORKSPACE, LLAMA3_ERR_CUDA.
+ */
+int llama3_attention_tree(const llama3_config* cfg, const void* q, const void* k_cache, const void* v_cache,
+                          int cache_cap, const int32_t* kv_lens, int max_len, const void* k_nodes,
+                          const void* v_nodes, const int32_t* parents, int batch, int n_nodes, void* out,
+                          void* ws, size_t ws_bytes, llama3_stream_t stream);
+
+/*
+ * The path of the tree that the target model confirms.  Node 0 is the token the
+ * sequence ended with (sampled, but not yet in the cache) and is always
+ * accepted; from an accepted node the path goes on to its child whose drafted
+ * token equals the target's token behind that node (the lowest such child).
+ * draft_ids, target_ids, parents: int32 [batch, n_nodes]; target_ids[b][t] is
+ * the target's choice behind node t (its argmax, or its draw: the tokens
+ * then follow the target's own law).
+ *   path [batch, n_nodes]: the accepted nodes in order, -1 behind them;
+ *   n_accepted [batch]; 0 where node 0 is not a root (parents[b][0] != -1);
+ *   next_ids [batch]: target_ids of the last accepted node, -1 without one;
+ *   kv_lens_out[b] = kv_lens[b] + n_accepted[b];
+ *   positions_out[b] = positions[b] + n_accepted[b] (both may be NULL).
+ * kv_lens_out may be kv_lens, positions_out may be positions.  All device
+ * int32, 4-byte aligned.  Errors: LLAMA3_ERR_ARG, LLAMA3_ERR_ALIGN.
+ */
+int llama3_tree_accept(const int32_t* draft_ids, const int32_t* target_ids, const int32_t* parents, int batch,
+                       int n_nodes, const int32_t* kv_lens, int32_t* path, int32_t* n_accepted,
+                       int32_t* next_ids, int32_t* kv_lens_out, const int32_t* positions,
+                       int32_t* positions_out, llama3_stream_t stream);
+
+/* One layer's cache with what eviction needs to know of its slots.
+ *   k, v      [batch, cap, KV, hd]
+ *   weights   float [batch, KV, cap]: softmax weight each slot has received
+ *   slot_pos  int32 [batch, KV, cap]: position of the token each slot holds
+ * Calls that do not evict take NULL for the last two. */
+typedef struct llama3_bounded_cache {
+  void* k;
+  void* v;
+  float* weights;
+  int32_t* slot_pos;
+} llama3_bounded_cache;
+
+/*
+ * Copies the accepted nodes' keys and values behind the cached rows, in every
+ * layer: cache row kv_lens[b] - n_accepted[b] + i of sequence b becomes node
+ * path[b][i], for i < n_accepted[b].  kv_lens as llama3_tree_accept left it
+ * (that is, with the accepted nodes counted).  nodes[l].k, .v: [batch,
+ * n_nodes, KV, hd]; caches[l].k, .v: [batch, cache_cap, KV, hd] (host arrays of
+ * n_layers structs).  Where caches[l].weights / .slot_pos are not NULL, the new
+ * slots start with weight 0 and with the positions
+ * positions[b] - n_accepted[b] + i (positions as llama3_tree_accept left it;
+ * NULL: the cache row itself).  A sequence whose rows do not fit the cache is
+ * left alone and reported as LLAMA3_ERR_ARG through llama3_device_status.
+ * Errors: LLAMA3_ERR_ARG, LLAMA3_ERR_ALIGN, LLAMA3_ERR_CUDA.
+ */
+int llama3_tree_commit(const llama3_config* cfg, const llama3_bounded_cache* nodes,
+                       const llama3_bounded_cache* caches, int cache_cap, int n_layers, int batch, int n_nodes,
+                       const int32_t* path, const int32_t* n_accepted, const int32_t* kv_lens,
+                       const int32_t* positions, llama3_stream_t stream);
+
+/* ---- bounded caches: eviction by accumulated attention weight ----
+ *
+ * A cache that may not grow keeps, per sequence and KV head, the most recent
+ * tokens and those that the attention has looked at most.  Keys are stored
+ * rotated, so a slot keeps its meaning wherever it is moved, and the order of
+ * the slots does not matter to the attention (no counterpart on the pages).
+ */
+
+/* Bytes of workspace that llama3_attention_observed needs. */
+int llama3_observe_workspace_size(const llama3_config* cfg, int batch, int seq, int max_len, size_t* bytes);
+
+/*
+ * Causal GQA attention that also records where it looked.  The chunk's own
+ * keys and values are in the cache already, in rows kv_lens[b] .. kv_lens[b] +
+ * seq - 1; row t of sequence b sees cache rows j <= kv_lens[b] + t:
+ *   out[b, t, h] = sum_j p[b,t,h,j] v_j,  p = softmax_j(q . k_j / sqrt(hd))
+ *   weights[b, g, j] = (j < kv_lens[b] ? weights_in[b, g, j] : 0)
+ *                      + sum over t and the query heads h of group g of p[b,t,h,j]
+ * for j < kv_lens[b] + seq_lens[b]; other entries of weights are not written.
+ * weights_in NULL: zeros; it may be weights itself.  weights, weights_in and
+ * slot_pos: [batch, KV, cache_cap].  q: [batch, seq, H, hd], out: [batch, seq,
+ * H*hd].  kv_lens: device int32 [batch] in [0, max_len] (NULL: max_len for
+ * all); max_len + seq <= cache_cap.  seq_lens: device int32 [batch] in [0, seq]
+ * (NULL: seq for all): rows t >= seq_lens[b] are padding, which gives zeros in
+ * out and no weight.  Values outside are clamped and reported as
+ * LLAMA3_ERR_ARG through llama3_device_status.  slot_pos (nullable): the
+ * chunk's slots get positions[b] + t (positions NULL: kv_lens[b] + t).
+ * The sums have a fixed order: equal inputs give equal bits.
+ * ws: llama3_observe_workspace_size(cfg, batch, seq, max_len) bytes.
+ * Errors: LLAMA3_ERR_ARG, LLAMA3_ERR_ALIGN (the int32 and float arrays 4-byte,
+ * all others 16-byte aligned), LLAMA3_ERR_WORKSPACE, LLAMA3_ERR_CUDA.
+ */
+int llama3_attention_observed(const llama3_config* cfg, const void* q, const void* k_cache,
+                              const void* v_cache, int cache_cap, int batch, int seq, const int32_t* kv_lens,
+                              const int32_t* seq_lens, int max_len, void* out, const float* weights_in,
+                              float* weights, const int32_t* positions, int32_t* slot_pos, void* ws,
+                              size_t ws_bytes, llama3_stream_t stream);
+
+/* Bytes of workspace that llama3_cache_evict needs. */
+int llama3_evict_workspace_size(const llama3_config* cfg, int n_layers, int batch, int max_len, int budget,
+                                size_t* bytes);
+
+/*
+ * Cuts caches to at most `budget` slots per (layer, sequence, KV head).  Where
+ * kv_lens[b] > budget, the kept slots are: those of the last `recent`
+ * positions (slot_pos >= positions[b] - recent, positions[b] being the number of
+ * tokens the sequence has seen), then the largest weights (a NaN before any
+ * number), the lower slot first among equals; budget of them in all.  A kept
+ * slot below `budget` stays where it is; the evicted slots below `budget`, in
+ * ascending order, receive the kept slots behind it, in ascending order: keys,
+ * values, weights and positions.  Sequences within the budget keep every slot.
+ * kv_lens_out[b] = min(kv_lens[b], budget) (may be kv_lens).
+ * src, dst: host arrays of n_layers structs, with capacities src_cap and
+ * dst_cap (>= min(budget, max_len)).  dst NULL: in place, moving only what
+ * fills a hole; otherwise dst's buffers receive the kept slots and must not
+ * overlap src's.  Rows behind kv_lens_out[b] are not written.  kv_lens,
+ * positions: device int32 [batch]; kv_lens in [0, max_len] (clamped and
+ * reported as LLAMA3_ERR_ARG through llama3_device_status otherwise).
+ * Errors: LLAMA3_ERR_ARG (recent outside [0, budget], ...), LLAMA3_ERR_ALIGN,
+ * LLAMA3_ERR_WORKSPACE, LLAMA3_ERR_CUDA.
+ */
+int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src, int src_cap,
+                       const llama3_bounded_cache* dst, int dst_cap, int n_layers, int batch,
+                       const int32_t* kv_lens, int max_len, int budget, int recent, const int32_t* positions,
+                       int32_t* kv_lens_out, void* ws, size_t ws_bytes, llama3_stream_t stream);
+
 /* ---- building blocks (the steps of the calls above, exposed for tests) ---- */
 
 /* y[r] = x[r] / sqrt(mean(x[r]^2) + eps) * w  ([S1] §5, [S2] §3.1); x rows at
@@ -389,7 +551,11 @@ enum llama3_kernel_kind {
   LLAMA3_KERNEL_LM_HEAD = 8,           /* LM-head GEMM + argmax                    */
   LLAMA3_KERNEL_NORM = 9,              /* RMSNorm                                  */
   LLAMA3_KERNEL_ELEMENTWISE = 10,      /* embedding, split-K reductions, misc.     */
-  LLAMA3_KERNEL_SAMPLE = 11            /* temperature / top-p draw                 */
+  LLAMA3_KERNEL_SAMPLE = 11,           /* temperature / top-p draw                 */
+  LLAMA3_KERNEL_TREE_ATTENTION = 12,   /* attention of a drafted tree              */
+  LLAMA3_KERNEL_OBSERVED_ATTENTION = 13, /* attention with accumulated weights     */
+  LLAMA3_KERNEL_EVICT = 14,            /* cache eviction                           */
+  LLAMA3_KERNEL_ACCEPT = 15            /* acceptance of a drafted path             */
 };
 
 /* Record start_events[i] / stop_events[i] (cudaEvent_t handles created by the

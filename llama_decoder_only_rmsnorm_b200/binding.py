@@ -31,6 +31,10 @@ class llama3_layer_weights(ctypes.Structure):
                 ("attention_norm", "wqkv", "wo", "ffn_norm", "w1", "w2", "w3")]
 
 
+class llama3_bounded_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "weights", "slot_pos")]
+
+
 class Llama3Error(RuntimeError):
     def __init__(self, name, status, cuda_error=0):
         self.status = status
@@ -44,6 +48,7 @@ class Llama3Error(RuntimeError):
 _lib = None
 _i, _ll, _sz, _p, _d = ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_double
 _cfgp, _wp = ctypes.POINTER(llama3_config), ctypes.POINTER(llama3_layer_weights)
+_cachep = ctypes.POINTER(llama3_bounded_cache)
 
 _SIGNATURES = {
     "llama3_init_rope_table": [_p, _i, _i, _d, _p],
@@ -71,6 +76,14 @@ _SIGNATURES = {
     "llama3_sample_top_p": [_p, _i, _ll, _i, ctypes.c_float, ctypes.c_float, ctypes.c_ulonglong, ctypes.c_ulonglong, _p, _p, _p],
     "llama3_generation_advance": [_p, _p, _p, _p, _p, _i, _i, _i, _ll, _p],
     "llama3_gather_rows": [_cfgp, _p, _ll, _i, _p, _i, _p, _p],
+    "llama3_tree_workspace_size": [_cfgp, _i, _i, _i, ctypes.POINTER(_sz)],
+    "llama3_attention_tree": [_cfgp, _p, _p, _p, _i, _p, _i, _p, _p, _p, _i, _i, _p, _p, _sz, _p],
+    "llama3_tree_accept": [_p, _p, _p, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p],
+    "llama3_tree_commit": [_cfgp, _cachep, _cachep, _i, _i, _i, _i, _p, _p, _p, _p, _p],
+    "llama3_observe_workspace_size": [_cfgp, _i, _i, _i, ctypes.POINTER(_sz)],
+    "llama3_attention_observed": [_cfgp, _p, _p, _p, _i, _i, _i, _p, _p, _i, _p, _p, _p, _p, _p, _p, _sz, _p],
+    "llama3_evict_workspace_size": [_cfgp, _i, _i, _i, _i, ctypes.POINTER(_sz)],
+    "llama3_cache_evict": [_cfgp, _cachep, _i, _cachep, _i, _i, _i, _p, _i, _i, _i, _p, _p, _p, _sz, _p],
     "llama3_set_launch_timer": [_i, _p, _p, _i],
     "llama3_launch_timer_used": [],
     "llama3_launch_count": [],
@@ -275,6 +288,84 @@ def llama3_attention(cfg, q, k_cache, v_cache, cache_cap, batch, seq, start_pos,
         _ptr(ws), ws_bytes, _stream(stream)))
 
 
+def make_bounded_caches(layers):
+    """Array of llama3_bounded_cache structs, one per layer, from dicts with k
+    and v (and, for eviction, weights and slot_pos) tensors.  The caller keeps
+    the tensors alive."""
+    layers = list(layers)
+    return (llama3_bounded_cache * len(layers))(*[
+        llama3_bounded_cache(*[None if c.get(n) is None else c[n].data_ptr()
+                               for n in ("k", "v", "weights", "slot_pos")]) for c in layers])
+
+
+def llama3_tree_workspace_size(cfg, batch, n_nodes, max_len):
+    n = ctypes.c_size_t(0)
+    _check("llama3_tree_workspace_size", lib().llama3_tree_workspace_size(ctypes.byref(cfg), batch, n_nodes, max_len,
+                                                                          ctypes.byref(n)))
+    return n.value
+
+
+def llama3_attention_tree(cfg, q, k_cache, v_cache, cache_cap, kv_lens, max_len, k_nodes, v_nodes, parents, batch,
+                          n_nodes, out, ws, ws_bytes, stream=None):
+    """Attention of a drafted tree (parents int32 [batch, n_nodes]) over the caches."""
+    _check("llama3_attention_tree", lib().llama3_attention_tree(
+        ctypes.byref(cfg), _ptr(q), _ptr(k_cache), _ptr(v_cache), cache_cap, _ptr(kv_lens), max_len, _ptr(k_nodes),
+        _ptr(v_nodes), _ptr(parents), batch, n_nodes, _ptr(out), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def llama3_tree_accept(draft_ids, target_ids, parents, batch, n_nodes, kv_lens, path, n_accepted, next_ids,
+                       kv_lens_out, positions=None, positions_out=None, stream=None):
+    """The confirmed path of a drafted tree; advances kv_lens (and positions)."""
+    _check("llama3_tree_accept", lib().llama3_tree_accept(
+        _ptr(draft_ids), _ptr(target_ids), _ptr(parents), batch, n_nodes, _ptr(kv_lens), _ptr(path),
+        _ptr(n_accepted), _ptr(next_ids), _ptr(kv_lens_out), _ptr(positions), _ptr(positions_out), _stream(stream)))
+
+
+def llama3_tree_commit(cfg, nodes, caches, cache_cap, batch, n_nodes, path, n_accepted, kv_lens, positions=None,
+                       stream=None):
+    """Copy the accepted nodes' rows into every layer's cache; nodes and caches
+    from make_bounded_caches, one struct per layer."""
+    if len(nodes) != len(caches):
+        raise ValueError("nodes and caches must have one struct per layer each")
+    _check("llama3_tree_commit", lib().llama3_tree_commit(
+        ctypes.byref(cfg), nodes, caches, cache_cap, len(caches), batch, n_nodes, _ptr(path), _ptr(n_accepted),
+        _ptr(kv_lens), _ptr(positions), _stream(stream)))
+
+
+def llama3_observe_workspace_size(cfg, batch, seq, max_len):
+    n = ctypes.c_size_t(0)
+    _check("llama3_observe_workspace_size", lib().llama3_observe_workspace_size(ctypes.byref(cfg), batch, seq,
+                                                                                max_len, ctypes.byref(n)))
+    return n.value
+
+
+def llama3_attention_observed(cfg, q, k_cache, v_cache, cache_cap, batch, seq, kv_lens, seq_lens, max_len, out,
+                              weights_in, weights, positions, slot_pos, ws, ws_bytes, stream=None):
+    """Causal attention that adds each slot's softmax weight to weights."""
+    _check("llama3_attention_observed", lib().llama3_attention_observed(
+        ctypes.byref(cfg), _ptr(q), _ptr(k_cache), _ptr(v_cache), cache_cap, batch, seq, _ptr(kv_lens),
+        _ptr(seq_lens), max_len, _ptr(out), _ptr(weights_in), _ptr(weights), _ptr(positions), _ptr(slot_pos),
+        _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def llama3_evict_workspace_size(cfg, n_layers, batch, max_len, budget):
+    n = ctypes.c_size_t(0)
+    _check("llama3_evict_workspace_size", lib().llama3_evict_workspace_size(ctypes.byref(cfg), n_layers, batch,
+                                                                            max_len, budget, ctypes.byref(n)))
+    return n.value
+
+
+def llama3_cache_evict(cfg, src, src_cap, dst, dst_cap, batch, kv_lens, max_len, budget, recent, positions,
+                       kv_lens_out, ws, ws_bytes, stream=None):
+    """Cut every layer's caches to the budget; src and dst from
+    make_bounded_caches (dst None: in place)."""
+    if dst is not None and len(dst) != len(src):
+        raise ValueError("src and dst must have one struct per layer each")
+    _check("llama3_cache_evict", lib().llama3_cache_evict(
+        ctypes.byref(cfg), src, src_cap, dst, dst_cap, len(src), batch, _ptr(kv_lens), max_len, budget, recent,
+        _ptr(positions), _ptr(kv_lens_out), _ptr(ws), ws_bytes, _stream(stream)))
+
+
 def llama3_status_string(status):
     return lib().llama3_status_string(status).decode()
 
@@ -308,7 +399,8 @@ def llama3_set_programmatic_launch(on):
 
 
 KERNEL_KINDS = {"gemm_qkv": 1, "gemm_wo": 2, "gemm_w13": 3, "gemm_w2": 4, "attention": 5, "decode_gemm": 6,
-                "decode_attention": 7, "lm_head": 8, "norm": 9, "elementwise": 10, "sample": 11}
+                "decode_attention": 7, "lm_head": 8, "norm": 9, "elementwise": 10, "sample": 11,
+                "tree_attention": 12, "observed_attention": 13, "evict": 14, "accept": 15}
 
 
 def llama3_set_launch_timer(kind, start_events, stop_events):

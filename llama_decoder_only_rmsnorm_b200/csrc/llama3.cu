@@ -5,6 +5,7 @@
 // every argument before launching anything, build TMA descriptors for the
 // tcgen05 kernels, carve the caller's workspace, and launch on the caller's
 // stream.  No device memory is allocated here.
+#include <limits.h>
 #include <math.h>
 #include <string.h>
 
@@ -13,6 +14,7 @@
 #include <mutex>
 #include <vector>
 
+#include "cache_ops.cuh"
 #include "common.cuh"
 #include "decode_attention.cuh"
 #include "flash_attention.cuh"
@@ -1436,3 +1438,5 @@ extern "C" int llama3_lm_head_argmax_noalloc(const llama3_config* cfg, const voi
   void* hn = static_cast<char*>(base) + keys_bytes;
   return lm_head_run(cfg, norm_w, w_out, h, rows, row_stride, ids_out, logits_out, hn, keys, st);
 }
+
+#include "cache_calls.cuh"
