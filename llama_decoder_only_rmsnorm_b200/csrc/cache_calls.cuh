@@ -7,61 +7,253 @@ namespace {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-struct TreeWorkspace {
-  size_t total;
+// The tensor-core kernels take bf16 heads of 32 and more; fp32, head_dim 16 and
+// groups of more query heads than a tile has rows go to the CUDA cores.
+bool rows_on_tc(const llama3_config* c) {
+  return c->dtype == LLAMA3_DTYPE_BF16 && g_kernel_path != 1 && c->head_dim >= 32 && c->n_heads / c->n_kv_heads <= 128;
+}
+// Query rows of a tile on the CUDA cores; a KV head of more query heads than that is refused.
+bool rows_supported(const llama3_config* c) { return rows_on_tc(c) || c->n_heads / c->n_kv_heads <= kSimtTile; }
+
+// How T query positions per sequence over at most max_keys cached rows are laid
+// out, and what the launch needs of the workspace.
+struct RowsPlan {
+  RowsShape rs;
+  bool tc, pair;
+  size_t ml, o, nlse, sums, total;
 };
-TreeWorkspace tree_layout(const llama3_config*, int, int, int) {
-  TreeWorkspace w;
-  w.total = 0;
-  return w;
+RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len) {
+  RowsPlan p;
+  memset(&p, 0, sizeof(p));
+  RowsShape& rs = p.rs;
+  p.tc = rows_on_tc(c);
+  rs.B = B; rs.T = T; rs.H = c->n_heads; rs.KV = c->n_kv_heads; rs.rep = c->n_heads / c->n_kv_heads;
+  rs.tile_rows = p.tc ? 128 : kSimtTile;
+  rs.qpt = std::max(1, rs.tile_rows / rs.rep);
+  rs.tiles = (T + rs.qpt - 1) / rs.qpt;
+  p.pair = p.tc && rs.tiles > 1;
+  rs.slots = p.pair ? 2 : 1;
+  rs.groups = (rs.tiles + rs.slots - 1) / rs.slots;
+  rs.key_shift = p.tc ? 7 : 6;
+  rs.max_len = max_len;
+  rs.scale_log2 = (float)(1.4426950408889634 / sqrt((double)c->head_dim));
+  // one CTA per SM for the tensor-core kernels, two of the others; no more than there is work for
+  const long long keys = (long long)max_len + (tree ? 0 : T);
+  const long long work = (long long)B * rs.groups * rs.KV * ((keys + (1 << rs.key_shift) - 1) >> rs.key_shift);
+  rs.G = (int)std::min((long long)num_sms() * (p.tc ? 1 : 2), work);
+  const size_t records = tree ? (size_t)B * rs.groups * rs.KV + rs.G : (size_t)2 * rs.G;
+  const size_t rows = records * rs.slots * rs.tile_rows;
+  size_t off = 0;
+  p.ml = off; off += up256(rows * 2 * 4);
+  p.o = off; off += up256(rows * c->head_dim * 4);
+  if (!tree) {
+    p.nlse = off; off += up256((size_t)B * rs.KV * rs.tiles * rs.tile_rows * 4);
+    p.sums = off; off += up256((size_t)2 * num_sms() * 2 * rs.tile_rows * 4);
+  }
+  p.total = rs.G > 0 ? off : 0;
+  return p;
 }
 
-struct ObserveWorkspace {
-  size_t lse, total;
+// q as 128-row tiles of 128 / rep positions x rep heads: {hd, rep, KV, T, B}.
+int make_map_rows(CUtensorMap* m, const void* q, const llama3_config* c, const RowsShape& rs) {
+  EncodeTiledFn enc;
+  L3_TRY(encode_fn(&enc));
+  const cuuint64_t hd = c->head_dim;
+  cuuint64_t dims[5] = {hd, (cuuint64_t)rs.rep, (cuuint64_t)rs.KV, (cuuint64_t)rs.T, (cuuint64_t)rs.B};
+  cuuint64_t strides[4] = {hd * 2, rs.rep * hd * 2, rs.H * hd * 2, rs.T * (rs.H * hd * 2)};
+  cuuint32_t box[5] = {64u, (cuuint32_t)rs.rep, 1u, (cuuint32_t)rs.qpt, 1u};
+  cuuint32_t es[5] = {1u, 1u, 1u, 1u, 1u};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(q), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    t_last_cuda = (int)r;
+    return LLAMA3_ERR_CUDA;
+  }
+  return LLAMA3_OK;
+}
+
+template <typename K>
+int opt_in_smem(K kern, int bytes, bool* done) {
+  int dev = 0;
+  L3_TRY(current_device(&dev));
+  if (!done[dev]) {
+    L3_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    done[dev] = true;
+  }
+  return LLAMA3_OK;
+}
+
+template <int HD, bool TREE, bool PAIR>
+int run_rows_tc_t(const llama3_config* c, const RowsPlan& p, const void* q, const void* kc, const void* vc, int cap,
+                  cudaStream_t st) {
+  const RowsShape& rs = p.rs;
+  const long long e = 2, keys = (long long)rs.max_len + (TREE ? 0 : rs.T);
+  CUtensorMap mq, mk, mv;
+  L3_TRY(make_map_rows(&mq, q, c, rs));
+  L3_TRY(make_map_4d(&mk, kc, HD, rs.KV, keys, rs.B, HD * e, rs.KV * HD * e, (long long)cap * rs.KV * HD * e));
+  L3_TRY(make_map_4d(&mv, vc, HD, rs.KV, keys, rs.B, HD * e, rs.KV * HD * e, (long long)cap * rs.KV * HD * e));
+  auto kern = rows_attention_kernel<HD, TREE, PAIR>;
+  constexpr int smem = RowsCfg<HD, PAIR>::SMEM_BYTES;
+  int dev = 0;
+  L3_TRY(current_device(&dev));
+  static bool attr_done[kMaxDevices], regs_ok[kMaxDevices];
+  if (!attr_done[dev]) {
+    L3_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    // the warpgroups' register shares have to fit the block's (see run_flash_attention_t)
+    cudaFuncAttributes fa;
+    L3_CUDA(cudaFuncGetAttributes(&fa, kern));
+    regs_ok[dev] = (long long)fa.numRegs * kFlashThreads >= 128LL * kFlashLowRegs + 256LL * kFlashHighRegs;
+    attr_done[dev] = true;
+  }
+  if (!regs_ok[dev]) return LLAMA3_ERR_UNSUPPORTED;
+  L3_LAUNCH(TREE ? LLAMA3_KERNEL_TREE_ATTENTION : LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
+            launch_k(kern, rs.G, kFlashThreads, smem, st, mq, mk, mv, rs, wait_ns()));
+  return launch_check();
+}
+
+template <typename T, int HD, bool TREE>
+int run_rows_simt_t(const RowsPlan& p, const void* q, const void* kc, const void* vc, int cap, cudaStream_t st) {
+  auto kern = rows_simt_kernel<T, HD, TREE>;
+  static bool done[kMaxDevices];
+  L3_TRY(opt_in_smem(kern, SimtCfg<HD>::ATT_BYTES, done));
+  L3_LAUNCH(TREE ? LLAMA3_KERNEL_TREE_ATTENTION : LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
+            launch_k(kern, p.rs.G, 256, SimtCfg<HD>::ATT_BYTES, st, p.rs, (const T*)q, (const T*)kc, (const T*)vc, cap));
+  return launch_check();
+}
+
+// The main pass over the cache for T = float or bf16.
+template <typename T, int HD, bool TREE>
+int run_rows(const llama3_config* c, const RowsPlan& p, const void* q, const void* kc, const void* vc, int cap,
+             cudaStream_t st) {
+  if constexpr (std::is_same<T, bf16>::value && HD >= 32) {
+    if (p.tc)
+      return p.pair ? run_rows_tc_t<HD, TREE, true>(c, p, q, kc, vc, cap, st)
+                    : run_rows_tc_t<HD, TREE, false>(c, p, q, kc, vc, cap, st);
+  }
+  return run_rows_simt_t<T, HD, TREE>(p, q, kc, vc, cap, st);
+}
+
+struct TreeArgs {
+  const void *q, *kc, *vc, *kn, *vn;
+  const int32_t *kv_lens, *parents;
+  int cap;
+  void *out, *ws;
 };
-ObserveWorkspace observe_layout(const llama3_config* c, int batch, int seq, int max_len) {
-  ObserveWorkspace w;
-  (void)max_len;
-  size_t off = 0;
-  w.lse = off; off += up256((size_t)batch * c->n_heads * seq * 4);
-  w.total = off;
-  return w;
+template <typename T, int HD>
+int run_tree(const llama3_config* c, RowsPlan& p, const TreeArgs& a, cudaStream_t st) {
+  RowsShape& rs = p.rs;
+  rs.kv_lens = a.kv_lens;
+  rs.out = a.out;
+  rs.part_ml = ws_at<float>(a.ws, p.ml);
+  rs.part_o = ws_at<float>(a.ws, p.o);
+  if (rs.G > 0) L3_TRY((run_rows<T, HD, true>(c, p, a.q, a.kc, a.vc, a.cap, st)));
+  L3_LAUNCH(LLAMA3_KERNEL_TREE_ATTENTION, st,
+            launch_k((tree_join_kernel<T, HD>), dim3(rs.B * rs.KV, (rs.T * rs.rep + kJoinWarps - 1) / kJoinWarps),
+                     32 * kJoinWarps, 0, st, rs, (const T*)a.q, (const T*)a.kn, (const T*)a.vn, a.parents));
+  return launch_check();
+}
+
+struct ObserveArgs {
+  const void *q, *kc, *vc;
+  const int32_t *kv_lens, *seq_lens, *positions;
+  const float* win;
+  float* wout;
+  int32_t* slot_pos;
+  int cap;
+  void *out, *ws;
+};
+template <typename T, int HD>
+int run_observe(const llama3_config* c, RowsPlan& p, const ObserveArgs& a, cudaStream_t st) {
+  RowsShape& rs = p.rs;
+  rs.kv_lens = a.kv_lens;
+  rs.seq_lens = a.seq_lens;
+  rs.out = a.out;
+  rs.part_ml = ws_at<float>(a.ws, p.ml);
+  rs.part_o = ws_at<float>(a.ws, p.o);
+  rs.nlse = ws_at<float>(a.ws, p.nlse);
+  L3_TRY((run_rows<T, HD, false>(c, p, a.q, a.kc, a.vc, a.cap, st)));
+  if (rs.G > 1) {
+    L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
+              launch_k((causal_join_kernel<T, HD>), dim3(rs.G - 1, (rs.slots * rs.tile_rows + 63) / 64),
+                       32 * kJoinWarps, 0, st, rs));
+    L3_TRY(launch_check());
+  }
+  WeightShape w;
+  memset(&w, 0, sizeof(w));
+  w.B = rs.B; w.S = rs.T; w.KV = rs.KV; w.rep = rs.rep; w.qpt = rs.qpt; w.tiles = rs.tiles; w.tile_rows = rs.tile_rows;
+  w.key_shift = rs.key_shift;
+  w.key_tiles = (rs.max_len + rs.T + (1 << w.key_shift) - 1) >> w.key_shift;
+  w.max_len = rs.max_len; w.cap = a.cap; w.scale_log2 = rs.scale_log2;
+  w.kv_lens = a.kv_lens; w.seq_lens = a.seq_lens; w.positions = a.positions;
+  w.nlse = rs.nlse; w.win = a.win; w.wout = a.wout; w.slot_pos = a.slot_pos;
+  w.part = ws_at<float>(a.ws, p.sums);
+  const long long most = (long long)w.B * w.key_tiles * w.KV * w.tiles;
+  w.G = (int)std::min((long long)num_sms() * (p.tc ? 1 : 2), most);
+  bool launched = false;
+  if constexpr (std::is_same<T, bf16>::value && HD >= 32) {
+    if (p.tc) {
+      CUtensorMap mq, mk;
+      L3_TRY(make_map_rows(&mq, a.q, c, rs));
+      L3_TRY(make_map_4d(&mk, a.kc, HD, rs.KV, (long long)rs.max_len + rs.T, rs.B, HD * 2, rs.KV * HD * 2,
+                         (long long)a.cap * rs.KV * HD * 2));
+      auto kern = slot_weights_kernel<HD>;
+      static bool done[kMaxDevices];
+      L3_TRY(opt_in_smem(kern, WeightCfg<HD>::SMEM_BYTES, done));
+      L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
+                launch_k(kern, w.G, 384, WeightCfg<HD>::SMEM_BYTES, st, mq, mk, w, wait_ns()));
+      L3_TRY(launch_check());
+      launched = true;
+    }
+  }
+  if (!launched) {
+    auto kern = slot_weights_simt_kernel<T, HD>;
+    static bool done[kMaxDevices];
+    L3_TRY(opt_in_smem(kern, SimtCfg<HD>::WGT_BYTES, done));
+    L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
+              launch_k(kern, w.G, 256, SimtCfg<HD>::WGT_BYTES, st, w, (const T*)a.q, (const T*)a.kc, rs.H));
+    L3_TRY(launch_check());
+  }
+  L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
+            launch_k(slot_weights_join_kernel, w.G - 1 + w.B, 128, 0, st, w));
+  return launch_check();
+}
+
+#define L3_FOR_HEADS(c, CALL)                                          \
+  ((c)->dtype == LLAMA3_DTYPE_F32                                      \
+       ? ((c)->head_dim == 16   ? CALL(float, 16)                      \
+          : (c)->head_dim == 32 ? CALL(float, 32)                      \
+          : (c)->head_dim == 64 ? CALL(float, 64)                      \
+          : (c)->head_dim == 96 ? CALL(float, 96)                      \
+                                : CALL(float, 128))                    \
+       : ((c)->head_dim == 16   ? CALL(bf16, 16)                       \
+          : (c)->head_dim == 32 ? CALL(bf16, 32)                       \
+          : (c)->head_dim == 64 ? CALL(bf16, 64)                       \
+          : (c)->head_dim == 96 ? CALL(bf16, 96)                       \
+                                : CALL(bf16, 128)))
+
+// Sizes that the kernels' 32-bit indexes hold.
+bool rows_in_range(const llama3_config* c, int batch, int rows, long long keys) {
+  const long long lim = 1LL << 30;
+  return keys < lim && (long long)batch * rows < lim && (long long)batch * rows * c->n_heads < lim &&
+         (long long)batch * c->n_kv_heads * ((keys + 63) / 64) < lim &&
+         (long long)rows * (c->n_heads / c->n_kv_heads) / kJoinWarps < 65535;
 }
 
 int check_tree_shape(const llama3_config* c, int batch, int nodes, int max_len) {
   L3_TRY(check_config(c));
   if (batch < 1 || nodes < 1 || nodes > kMaxTreeNodes || max_len < 0) return LLAMA3_ERR_ARG;
-  return LLAMA3_OK;
+  if (!rows_in_range(c, batch, nodes, max_len)) return LLAMA3_ERR_ARG;
+  return rows_supported(c) ? LLAMA3_OK : LLAMA3_ERR_UNSUPPORTED;
 }
-
-template <typename T>
-int run_tree_simt(const llama3_config* c, const void* q, const void* kc, const void* vc, int cap, const int32_t* lens,
-                  int max_len, const void* kn, const void* vn, const int32_t* parents, int B, int nodes, void* out,
-                  cudaStream_t st) {
-  const long long warps = (long long)B * nodes * c->n_heads;
-  L3_LAUNCH(LLAMA3_KERNEL_TREE_ATTENTION, st,
-            launch_k((tree_attention_simt_kernel<T>), blocks_for(warps * 32, 256), 256, 0, st, (const T*)q,
-                     (const T*)kc, (const T*)vc, (const T*)kn, (const T*)vn, lens, parents, (T*)out, B, nodes,
-                     c->n_heads, c->n_kv_heads, c->head_dim, cap, max_len, (float)(1.0 / sqrt((double)c->head_dim))));
-  return launch_check();
-}
-
-template <typename T>
-int run_observe_simt(const llama3_config* c, const void* q, const void* kc, const void* vc, int cap, int B, int S,
-                     const int32_t* lens, const int32_t* seq_lens, int max_len, void* out, const float* win,
-                     float* wout, const int32_t* positions, int32_t* slot_pos, float* lse, cudaStream_t st) {
-  const float scale = (float)(1.0 / sqrt((double)c->head_dim));
-  const int H = c->n_heads, KV = c->n_kv_heads, hd = c->head_dim;
-  L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
-            launch_k((observed_attention_simt_kernel<T>), blocks_for((long long)B * S * H * 32, 256), 256, 0, st,
-                     (const T*)q, (const T*)kc, (const T*)vc, lens, seq_lens, (T*)out, lse, B, S, H, KV, hd, cap,
-                     max_len, scale));
-  L3_TRY(launch_check());
-  L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
-            launch_k((observed_weights_simt_kernel<T>), blocks_for((long long)B * KV * (max_len + S) * 32, 256), 256,
-                     0, st, (const T*)q, (const T*)kc, lens, seq_lens, (const float*)lse, win, wout, positions,
-                     slot_pos, B, S, H, KV, hd, cap, max_len, scale));
-  return launch_check();
+int check_observe_shape(const llama3_config* c, int batch, int seq, int max_len) {
+  L3_TRY(check_config(c));
+  if (batch < 1 || seq < 1 || max_len < 0) return LLAMA3_ERR_ARG;
+  const long long lim = 1LL << 30, keys = (long long)max_len + seq;
+  if (keys >= lim || (long long)batch * seq >= lim || (long long)batch * seq * c->n_heads >= lim ||
+      (long long)batch * c->n_kv_heads * ((keys + 63) / 64) >= lim)
+    return LLAMA3_ERR_ARG;
+  return rows_supported(c) ? LLAMA3_OK : LLAMA3_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -71,7 +263,7 @@ extern "C" {
 int llama3_tree_workspace_size(const llama3_config* cfg, int batch, int n_nodes, int max_len, size_t* bytes) {
   L3_TRY(check_tree_shape(cfg, batch, n_nodes, max_len));
   if (!bytes) return LLAMA3_ERR_ARG;
-  *bytes = tree_layout(cfg, batch, n_nodes, max_len).total;
+  *bytes = plan_rows(cfg, true, batch, n_nodes, max_len).total;
   return LLAMA3_OK;
 }
 
@@ -85,21 +277,20 @@ int llama3_attention_tree(const llama3_config* cfg, const void* q, const void* k
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_nodes) || !aligned16(v_nodes) ||
       !aligned16(out) || !aligned4(kv_lens) || !aligned4(parents))
     return LLAMA3_ERR_ALIGN;
-  const TreeWorkspace L = tree_layout(cfg, batch, n_nodes, max_len);
-  if (L.total && (!ws || ws_bytes < L.total)) return LLAMA3_ERR_WORKSPACE;
+  RowsPlan p = plan_rows(cfg, true, batch, n_nodes, max_len);
+  if (p.total && (!ws || ws_bytes < p.total)) return LLAMA3_ERR_WORKSPACE;
   if (!aligned16(ws)) return LLAMA3_ERR_ALIGN;
+  const TreeArgs a = {q, k_cache, v_cache, k_nodes, v_nodes, kv_lens, parents, cache_cap, out, ws};
   cudaStream_t st = (cudaStream_t)stream;
-  return cfg->dtype == LLAMA3_DTYPE_F32
-             ? run_tree_simt<float>(cfg, q, k_cache, v_cache, cache_cap, kv_lens, max_len, k_nodes, v_nodes, parents,
-                                    batch, n_nodes, out, st)
-             : run_tree_simt<bf16>(cfg, q, k_cache, v_cache, cache_cap, kv_lens, max_len, k_nodes, v_nodes, parents,
-                                   batch, n_nodes, out, st);
+#define L3_TREE(T, HD) run_tree<T, HD>(cfg, p, a, st)
+  return L3_FOR_HEADS(cfg, L3_TREE);
+#undef L3_TREE
 }
 
 int llama3_observe_workspace_size(const llama3_config* cfg, int batch, int seq, int max_len, size_t* bytes) {
-  L3_TRY(check_config(cfg));
-  if (!bytes || batch < 1 || seq < 1 || max_len < 0) return LLAMA3_ERR_ARG;
-  *bytes = observe_layout(cfg, batch, seq, max_len).total;
+  L3_TRY(check_observe_shape(cfg, batch, seq, max_len));
+  if (!bytes) return LLAMA3_ERR_ARG;
+  *bytes = plan_rows(cfg, false, batch, seq, max_len).total;
   return LLAMA3_OK;
 }
 
@@ -108,23 +299,22 @@ int llama3_attention_observed(const llama3_config* cfg, const void* q, const voi
                               int max_len, void* out, const float* weights_in, float* weights,
                               const int32_t* positions, int32_t* slot_pos, void* ws, size_t ws_bytes,
                               llama3_stream_t stream) {
-  L3_TRY(check_config(cfg));
-  if (!q || !k_cache || !v_cache || !out || !weights || batch < 1 || seq < 1 || max_len < 0) return LLAMA3_ERR_ARG;
+  L3_TRY(check_observe_shape(cfg, batch, seq, max_len));
+  if (!q || !k_cache || !v_cache || !out || !weights) return LLAMA3_ERR_ARG;
   if ((long long)max_len + seq > cache_cap) return LLAMA3_ERR_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned4(kv_lens) ||
       !aligned4(seq_lens) || !aligned4(weights_in) || !aligned4(weights) || !aligned4(positions) ||
       !aligned4(slot_pos))
     return LLAMA3_ERR_ALIGN;
-  const ObserveWorkspace L = observe_layout(cfg, batch, seq, max_len);
-  if (!ws || ws_bytes < L.total) return LLAMA3_ERR_WORKSPACE;
+  RowsPlan p = plan_rows(cfg, false, batch, seq, max_len);
+  if (!ws || ws_bytes < p.total) return LLAMA3_ERR_WORKSPACE;
   if (!aligned16(ws)) return LLAMA3_ERR_ALIGN;
+  const ObserveArgs a = {q,          k_cache, v_cache,  kv_lens,   seq_lens, positions,
+                         weights_in, weights, slot_pos, cache_cap, out,      ws};
   cudaStream_t st = (cudaStream_t)stream;
-  float* lse = ws_at<float>(ws, L.lse);
-  return cfg->dtype == LLAMA3_DTYPE_F32
-             ? run_observe_simt<float>(cfg, q, k_cache, v_cache, cache_cap, batch, seq, kv_lens, seq_lens, max_len,
-                                       out, weights_in, weights, positions, slot_pos, lse, st)
-             : run_observe_simt<bf16>(cfg, q, k_cache, v_cache, cache_cap, batch, seq, kv_lens, seq_lens, max_len,
-                                      out, weights_in, weights, positions, slot_pos, lse, st);
+#define L3_OBSERVE(T, HD) run_observe<T, HD>(cfg, p, a, st)
+  return L3_FOR_HEADS(cfg, L3_OBSERVE);
+#undef L3_OBSERVE
 }
 
 int llama3_evict_workspace_size(const llama3_config* cfg, int n_layers, int batch, int max_len, int budget,

@@ -28,156 +28,6 @@ __device__ __forceinline__ int cached_len(const int32_t* lens, int b, int max_le
   return max(0, min(n, max_len));
 }
 
-// Whether node t hangs on the cache: its parents, followed up, end at -1.  A
-// parent below -1 marks padding (the node and all below it are dead); a parent
-// at or behind its child is an error, and counts as padding.
-__device__ __forceinline__ bool tree_live(const int32_t* par, int t) {
-  for (int c = t;;) {
-    const int p = par[c];
-    if (p == -1) return true;
-    if (p < -1) return false;
-    if (p >= c) {
-      record_error(LLAMA3_ERR_ARG);
-      return false;
-    }
-    c = p;
-  }
-}
-
-// One query row against a list of keys, a warp per row: lane l owns dims l, l + 32, ...
-template <typename T>
-struct WarpRow {
-  float q[4], acc[4], m, l;
-  int hd, lane;
-  float scale;
-  __device__ __forceinline__ void start(const T* qr, int hd_, float scale_) {
-    hd = hd_;
-    scale = scale_;
-    lane = threadIdx.x & 31;
-    m = -INFINITY;
-    l = 0.f;
-    for (int i = 0; i < 4; ++i) {
-      const int d = lane + 32 * i;
-      q[i] = d < hd ? to_f(qr[d]) : 0.f;
-      acc[i] = 0.f;
-    }
-  }
-  __device__ __forceinline__ void key(const T* kr, const T* vr) {
-    float s = 0.f;
-    for (int i = 0; i < 4; ++i) {
-      const int d = lane + 32 * i;
-      if (d < hd) s = fmaf(q[i], to_f(kr[d]), s);
-    }
-    s = warp_sum(s) * scale;
-    const float mn = fmaxf(m, s);
-    const float corr = m == -INFINITY ? 0.f : expf(m - mn);
-    const float p = s == -INFINITY ? 0.f : expf(s - mn);
-    l = l * corr + p;
-    for (int i = 0; i < 4; ++i) {
-      const int d = lane + 32 * i;
-      acc[i] = acc[i] * corr + (d < hd ? p * to_f(vr[d]) : 0.f);
-    }
-    m = mn;
-  }
-  __device__ __forceinline__ void store(T* o, bool zero) const {
-    for (int i = 0; i < 4; ++i) {
-      const int d = lane + 32 * i;
-      if (d < hd) o[d] = from_f<T>(zero ? 0.f : acc[i] / l);
-    }
-  }
-};
-
-// ---- tree attention, one warp per (b, node, query head) ---------------------
-template <typename T>
-__global__ void tree_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,
-                                           const T* __restrict__ kn, const T* __restrict__ vn,
-                                           const int32_t* __restrict__ kv_lens, const int32_t* __restrict__ parents,
-                                           T* __restrict__ out, int B, int nodes, int H, int KV, int hd, int cap,
-                                           int max_len, float scale) {
-  griddep_wait_and_release();
-  const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (w >= (long long)B * nodes * H) return;
-  const int h = (int)(w % H), t = (int)((w / H) % nodes), b = (int)(w / ((long long)H * nodes));
-  const int g = h / (H / KV);
-  const int32_t* par = parents + (size_t)b * nodes;
-  const int len = cached_len(kv_lens, b, max_len);
-  const size_t row = ((size_t)b * nodes + t) * H + h;
-  WarpRow<T> r;
-  r.start(q + row * hd, hd, scale);
-  const bool live = tree_live(par, t);
-  if (live) {
-    for (int j = 0; j < len; ++j) {
-      const size_t at = (((size_t)b * cap + j) * KV + g) * hd;
-      r.key(kc + at, vc + at);
-    }
-    for (int a = t; a >= 0; a = par[a]) {
-      const size_t at = (((size_t)b * nodes + a) * KV + g) * hd;
-      r.key(kn + at, vn + at);
-    }
-  }
-  r.store(out + row * hd, !live);
-}
-
-// ---- observed attention -----------------------------------------------------
-// First the attention itself, one warp per (b, t, query head), leaving each
-// row's log-sum-exp; then one warp per (b, KV head, slot) adds up the weights
-// exp(s - lse) of the rows that see the slot, in a fixed order.
-template <typename T>
-__global__ void observed_attention_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc,
-                                               const T* __restrict__ vc, const int32_t* __restrict__ kv_lens,
-                                               const int32_t* __restrict__ seq_lens, T* __restrict__ out,
-                                               float* __restrict__ lse, int B, int S, int H, int KV, int hd, int cap,
-                                               int max_len, float scale) {
-  griddep_wait_and_release();
-  const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (w >= (long long)B * S * H) return;
-  const int h = (int)(w % H), t = (int)((w / H) % S), b = (int)(w / ((long long)H * S));
-  const int g = h / (H / KV);
-  const int len = cached_len(kv_lens, b, max_len);
-  const bool live = t < cached_len(seq_lens, b, S);
-  const size_t row = ((size_t)b * S + t) * H + h;
-  WarpRow<T> r;
-  r.start(q + row * hd, hd, scale);
-  for (int j = 0; live && j <= len + t; ++j) {
-    const size_t at = (((size_t)b * cap + j) * KV + g) * hd;
-    r.key(kc + at, vc + at);
-  }
-  r.store(out + row * hd, !live);
-  if (live && r.lane == 0) lse[((size_t)b * H + h) * S + t] = r.m + logf(r.l);
-}
-
-template <typename T>
-__global__ void observed_weights_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc,
-                                             const int32_t* __restrict__ kv_lens, const int32_t* __restrict__ seq_lens,
-                                             const float* __restrict__ lse, const float* win, float* wout,
-                                             const int32_t* __restrict__ positions, int32_t* __restrict__ slot_pos,
-                                             int B, int S, int H, int KV, int hd, int cap, int max_len, float scale) {
-  griddep_wait_and_release();
-  const int lane = threadIdx.x & 31;
-  const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int slots = max_len + S;
-  if (w >= (long long)B * KV * slots) return;
-  const int j = (int)(w % slots), g = (int)((w / slots) % KV), b = (int)(w / ((long long)slots * KV));
-  const int len = cached_len(kv_lens, b, max_len), n = cached_len(seq_lens, b, S);
-  if (j >= len + n) return;
-  const int rep = H / KV;
-  const T* kr = kc + (((size_t)b * cap + j) * KV + g) * hd;
-  float sum = 0.f;
-  const int t0 = max(0, j - len);
-  for (int i = lane; i < (n - t0) * rep; i += 32) {
-    const int t = t0 + i / rep, h = g * rep + i % rep;
-    const T* qr = q + (((size_t)b * S + t) * H + h) * hd;
-    float s = 0.f;
-    for (int d = 0; d < hd; ++d) s = fmaf(to_f(qr[d]), to_f(kr[d]), s);
-    sum += expf(s * scale - lse[((size_t)b * H + h) * S + t]);
-  }
-  sum = warp_sum(sum);
-  if (lane) return;
-  const size_t at = ((size_t)b * KV + g) * cap + j;
-  wout[at] = (win && j < len ? win[at] : 0.f) + sum;
-  if (slot_pos && j >= len) slot_pos[at] = (positions ? positions[b] : len) + j - len;
-}
-
 // ---- eviction ---------------------------------------------------------------
 struct EvictLayer {
   const uint4 *k, *v;

@@ -1,0 +1,119 @@
+// flat_plan.cuh -- equal shares of ragged work, planned on the device.
+//
+// The cache operators work on segments (a sequence, a KV head and some query
+// rows or key slots) of n tiles each, where n depends on lengths that only the
+// device knows.  Laid end to end, every segment of n > 0 tiles takes n +
+// kFlatLead units of cost (kFlatLead stands for a segment's own start and
+// end); CTA c of G takes the units [c * per, (c + 1) * per), per = ceil(total /
+// G), so all CTAs carry the same load whatever the lengths are, and a segment
+// that crosses a border is cut into pieces there.  Every warp derives the plan
+// from the lengths alone, in the same way, so nothing is communicated.
+//
+// Items are what has a length (a sequence, or a sequence's query block); each
+// item stands for `mult` segments of the same n.  NOf is a functor int(int item).
+#pragma once
+#include "common.cuh"
+
+namespace l3 {
+
+// A segment's start and end (query load, first loads in flight, the result's
+// store) cost about as much as this many of its tiles.
+constexpr int kFlatLead = 2;
+
+__device__ __forceinline__ int flat_cost(int n) { return n > 0 ? n + kFlatLead : 0; }
+
+// Cost of all items; every lane gets it.  Whole warp.
+template <class NOf>
+__device__ __forceinline__ long long flat_total(int items, int mult, const NOf& n_of) {
+  long long t = 0;
+  for (int i = threadIdx.x & 31; i < items; i += 32) t += flat_cost(n_of(i));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t * mult;
+}
+
+// One segment: segment `sub` of `item`, n tiles, at cost units s0 .. s0 + n + kFlatLead - 1.
+struct FlatSeg {
+  int item, sub, n;
+  long long s0;
+  __device__ __forceinline__ long long end() const { return s0 + n + kFlatLead; }
+  // The tiles [w0, w1) of this segment within the units [a, e); false if there are none.
+  __device__ __forceinline__ bool cut(long long a, long long e, int& w0, int& w1) const {
+    w0 = (int)max(0LL, a - s0 - kFlatLead);
+    w1 = (int)(min(e, end()) - s0) - kFlatLead;
+    return w1 > w0;
+  }
+};
+
+// The segment that unit `pos` (< total) lies in.  Whole warp.
+template <class NOf>
+__device__ __forceinline__ FlatSeg flat_seek(int items, int mult, const NOf& n_of, long long pos) {
+  const int lane = threadIdx.x & 31;
+  long long base = 0;
+  FlatSeg s;
+  s.item = s.sub = s.n = 0;
+  s.s0 = 0;
+  for (int i0 = 0; i0 < items; i0 += 32) {
+    const int n = i0 + lane < items ? n_of(i0 + lane) : 0;
+    const long long own = (long long)flat_cost(n) * mult;
+    long long incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > pos);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      s.item = i0 + l;
+      s.n = __shfl_sync(0xffffffffu, n, l);
+      const long long start = base + __shfl_sync(0xffffffffu, incl - own, l);
+      s.sub = (int)((pos - start) / flat_cost(s.n));
+      s.s0 = start + (long long)s.sub * flat_cost(s.n);
+      return s;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return s;
+}
+
+// The pieces of one CTA, in order.
+template <class NOf>
+struct FlatRun {
+  FlatSeg seg;
+  long long a, e;
+  int items, mult;
+  bool more;
+  // Whole warp.
+  __device__ __forceinline__ void start(int items_, int mult_, const NOf& n_of, int c, int G) {
+    items = items_;
+    mult = mult_;
+    const long long total = flat_total(items, mult, n_of);
+    const long long per = (total + G - 1) / G;
+    a = per * c;
+    e = min(a + per, total);
+    more = a < e;
+    if (more) seg = flat_seek(items, mult, n_of, a);
+  }
+  // The next piece, or false at the end of the run (any lane, no communication).
+  __device__ __forceinline__ bool next(const NOf& n_of, FlatSeg& s, int& w0, int& w1) {
+    while (more) {
+      s = seg;
+      const bool some = s.cut(a, e, w0, w1);
+      seg.s0 = s.end();
+      if (seg.s0 >= e) {
+        more = false;
+      } else if (++seg.sub == mult) {
+        seg.sub = 0;
+        do {
+          ++seg.item;
+          seg.n = n_of(seg.item);
+        } while (seg.n == 0);   // ends: units below e <= total are left
+      }
+      if (some) return true;
+    }
+    return false;
+  }
+};
+
+}  // namespace l3

@@ -12,12 +12,14 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "cache_ops.cuh"
 #include "common.cuh"
 #include "decode_attention.cuh"
 #include "flash_attention.cuh"
+#include "rows_simt.cuh"
 #include "sampling.cuh"
 #include "simt.cuh"
 #include "tc_gemm.cuh"

@@ -1,0 +1,747 @@
+// rows_attention.cuh -- attention of several query rows per sequence over a
+// ragged cache, on tcgen05: the main kernel of tree attention (a drafted tree's
+// nodes over the cached rows) and of observed attention (a chunk's rows,
+// causal, leaving each row's log-sum-exp).
+//
+//  * The rows of one KV head are its sequence's query positions times the rep =
+//    H / KV query heads that share the head: row t * rep + j is position t,
+//    head g * rep + j.  A 128-row tile holds 128 / rep whole positions (one 5-D
+//    TMA box of q), so GQA heads fill the tensor core's rows even for a few
+//    positions, and every K/V tile is read once for up to 256 rows.
+//  * PAIR = true: a CTA works on two row tiles (slots) at once, each with its
+//    own softmax warpgroup; both use the same K/V tile.  PAIR = false, for at
+//    most 128 rows per KV head: the two warpgroups take alternate key tiles of
+//    the one row tile, so one's softmax hides behind the other's products, and
+//    join their (m, l, O) at the end of the piece through TMEM, in which both can
+//    read the same lanes.
+//  * Work is cut into equal shares over the CTAs by flat_plan.cuh: a long cache
+//    of one sequence spreads over the whole GPU, ragged batches stay balanced.
+//    A cut piece leaves a record (m, l, O) per row for the kernels below.
+//  * Within a tile: S = Q K^T (M = 128 rows, N = 128 keys) and O += P V with P
+//    in TMEM, one softmax thread per row, lazy rescaling, P handed over in two
+//    halves: the same scheme and register split as flash_attention.cuh.
+//  * V rows behind the sequence are zeroed in shared memory before the product
+//    (their probability is 0, but 0 x NaN is NaN), so the cache may hold
+//    anything there.
+#pragma once
+#include "cache_ops.cuh"
+#include "flash_attention.cuh"
+#include "flat_plan.cuh"
+
+namespace l3 {
+
+// The row and key tiles of a launch, for the main kernels and for those that join
+// their records.
+struct RowsShape {
+  int B, T, H, KV, rep;              // T query positions per sequence
+  int qpt, tiles, tile_rows;         // positions per row tile, row tiles, rows of a tile (128 or 64)
+  int slots, groups;                 // row tiles that a CTA works on together, and groups of them
+  int key_shift;                     // log2 of a key tile (7 or 6)
+  int G, max_len;                    // CTAs of the main kernel
+  float scale_log2;                  // log2(e) / sqrt(hd)
+  const int32_t *kv_lens, *seq_lens;
+  float *part_ml, *part_o;           // records: [id][row][2] and [id][hd/4][row][4], slots * tile_rows rows
+  float* nlse;                       // observed: minus the rows' log-sum-exp (log2), [B * KV][tiles][tile_rows]
+  void* out;
+};
+
+// Key tiles of an item.  Tree: item = sequence.  Causal: item = sequence and group.
+template <bool TREE>
+struct RowsTiles {
+  const RowsShape& rs;
+  __device__ __forceinline__ int operator()(int i) const {
+    const int up = (1 << rs.key_shift) - 1;
+    if (TREE) return (cached_len(rs.kv_lens, i, rs.max_len) + up) >> rs.key_shift;
+    const int b = i / rs.groups, t0 = (i % rs.groups) * rs.qpt * rs.slots;
+    const int live = cached_len(rs.seq_lens, b, rs.T);
+    if (t0 >= live) return 0;
+    return (cached_len(rs.kv_lens, b, rs.max_len) + min(live, t0 + rs.qpt * rs.slots) + up) >> rs.key_shift;
+  }
+  __device__ __forceinline__ int items() const { return TREE ? rs.B : rs.B * rs.groups; }
+  __device__ __forceinline__ int mult() const { return TREE ? rs.KV * rs.groups : rs.KV; }
+  __device__ __forceinline__ void where(const FlatSeg& s, int& b, int& grp, int& g) const {
+    b = TREE ? s.item : s.item / rs.groups;
+    grp = TREE ? s.sub / rs.KV : s.item % rs.groups;
+    g = s.sub % rs.KV;
+  }
+  // Record of the piece of segment s that the CTA c, whose run begins at unit a,
+  // works on.  Tree: every piece has one, and the segment's number plus the
+  // CTA's is another for each.  Causal: only the pieces of cut segments, which
+  // lie at the ends of a CTA's run.
+  __device__ __forceinline__ int record(const FlatSeg& s, int c, long long a) const {
+    return TREE ? s.item * mult() + s.sub + c : 2 * c + (s.s0 < a ? 0 : 1);
+  }
+};
+
+template <int HD, bool PAIR>
+struct RowsCfg {
+  static constexpr int CHUNKS = (HD + 63) / 64;
+  static constexpr int TILE = 128 * 128;               // 128 rows of 64 bf16
+  static constexpr int Q_BYTES = CHUNKS * TILE, KV_BYTES = CHUNKS * TILE;
+  static constexpr int NQ = PAIR ? 2 : 1;
+  static constexpr int RING0 = (232448 - 1024 - 1024 - 2048 - 8 * 2048 - NQ * Q_BYTES) / KV_BYTES;
+  static constexpr int RING = RING0 > 8 ? 8 : RING0;   // K and V tiles in flight
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_RING = NQ * Q_BYTES;
+  static constexpr int OFF_STAGE = OFF_RING + RING * KV_BYTES;   // 2 KB per softmax warp
+  static constexpr int OFF_ML = OFF_STAGE + 8 * 2048;            // [slot][128] x (m, l)
+  static constexpr int OFF_BAR = OFF_ML + 2048;
+  static constexpr int N_BARS = 4 + 2 * RING + 8 + 2;
+  static constexpr int SMEM_BYTES = 1024 + OFF_BAR + N_BARS * 8 + 16;
+  static_assert(SMEM_BYTES <= 232448 && RING >= 4, "shared memory");
+  static_assert(HD % 32 == 0 && HD <= 128, "head_dim");
+};
+
+// 2^x for two x <= 0 as exp2_poly2, with a polynomial of degree 5 (this
+// project's own fit, max relative error 2.4e-7): the accumulated weights and the
+// row sums that they are divided by are fp32 results.
+__device__ __forceinline__ void exp2_poly2_fine(float x0, float x1, float& y0, float& y1) {
+  const float shift = 12582912.0f;  // 1.5 * 2^23
+  const uint64_t x = f2_pack(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
+  const uint64_t t = f2_add(x, f2_pack(shift, shift));
+  const uint64_t f = f2_fma(f2_add(t, f2_pack(-shift, -shift)), f2_pack(-1.0f, -1.0f), x);
+  uint64_t p = f2_pack(0.001327647129073739f, 0.001327647129073739f);
+  p = f2_fma(p, f, f2_pack(0.009675541892647743f, 0.009675541892647743f));
+  p = f2_fma(p, f, f2_pack(0.05550713092088699f, 0.05550713092088699f));
+  p = f2_fma(p, f, f2_pack(0.24022120237350464f, 0.24022120237350464f));
+  p = f2_fma(p, f, f2_pack(0.6931469440460205f, 0.6931469440460205f));
+  p = f2_fma(p, f, f2_pack(1.0000001192092896f, 1.0000001192092896f));
+  float p0, p1, t0, t1;
+  f2_unpack(p, p0, p1);
+  f2_unpack(t, t0, t1);
+  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+}
+
+// p = 2^(s * scl - m) for 32 scores in place and their sum; the FMA pipe takes
+// 4 of 16 pairs of an unmasked row (FINE: with the fine polynomial).
+template <bool MASKED, bool FINE>
+__device__ __forceinline__ void rows_exp(uint32_t (&r)[32], float scl, float neg_m, float& sa, float& sb) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x0, x1, p0, p1;
+    fma2(x0, x1, __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), scl, scl, neg_m, neg_m);
+    if (!MASKED && (i & 7) < 2) {
+      if (FINE) exp2_poly2_fine(x0, x1, p0, p1); else exp2_poly2(x0, x1, p0, p1);
+    } else {
+      p0 = ex2_approx(x0);
+      p1 = ex2_approx(x1);
+    }
+    add2(sa, sb, p0, p1);
+    r[2 * i] = __float_as_uint(p0);
+    r[2 * i + 1] = __float_as_uint(p1);
+  }
+}
+template <bool MASKED, bool FINE>
+__device__ __forceinline__ float rows_exp_half(uint32_t (&ra)[32], uint32_t (&rb)[32], float scl, float neg_m,
+                                               uint32_t taddr) {
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  rows_exp<MASKED, FINE>(ra, scl, neg_m, s0, s1);
+  rows_exp<MASKED, FINE>(rb, scl, neg_m, s2, s3);
+  flash_pack_store(ra, taddr);
+  flash_pack_store(rb, taddr + 16);
+  return (s0 + s1) + (s2 + s3);
+}
+
+struct RowsBars {
+  uint64_t *q_full, *q_empty, *full, *empty, *s_full, *p_half, *p_full, *o_done, *merge;
+};
+
+// The order in which a piece of n key tiles uses its K and V tiles, which is the
+// order of their loads: f(is_v, tile).
+//   PAIR:  K0 V0 K1 V1 ...       (V_j is released before K_j+1)
+//   else:  K0 K1 V0 K2 V1 K3 ... (the warpgroups are one tile apart)
+template <bool PAIR, class F>
+__device__ __forceinline__ bool rows_ring_order(int n, const F& f) {
+  if (!f(false, 0)) return false;
+  if (!PAIR && n > 1 && !f(false, 1)) return false;
+  constexpr int ahead = PAIR ? 1 : 2;
+  for (int j = 0; j < n; ++j) {
+    if (!f(true, j)) return false;
+    if (j + ahead < n && !f(false, j + ahead)) return false;
+  }
+  return true;
+}
+
+template <int HD, bool TREE, bool PAIR>
+__global__ void __launch_bounds__(kFlashThreads, 1)
+    rows_attention_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                          const __grid_constant__ CUtensorMap mapV, const __grid_constant__ RowsShape rs,
+                          const unsigned long long wait_ns) {
+  using C = RowsCfg<HD, PAIR>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  RowsBars bars;
+  bars.q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  bars.q_empty = bars.q_full + 2;
+  bars.full = bars.q_empty + 2;
+  bars.empty = bars.full + C::RING;
+  bars.s_full = bars.empty + C::RING;
+  bars.p_half = bars.s_full + 2;
+  bars.p_full = bars.p_half + 2;
+  bars.o_done = bars.p_full + 2;
+  bars.merge = bars.o_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars.merge + 2);
+
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars.q_full[s], 1); mbar_init(&bars.q_empty[s], 1);
+      mbar_init(&bars.s_full[s], 1); mbar_init(&bars.o_done[s], 1);
+      mbar_init(&bars.p_half[s], 128); mbar_init(&bars.p_full[s], 128);
+      mbar_init(&bars.merge[s], 256);
+    }
+    for (int s = 0; s < C::RING; ++s) { mbar_init(&bars.full[s], 1); mbar_init(&bars.empty[s], 1); }
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&mapQ); prefetch_tensormap(&mapK); prefetch_tensormap(&mapV);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const RowsTiles<TREE> tiles_of{rs};
+  FlatRun<RowsTiles<TREE>> run;
+  FlatSeg seg;
+  int w0, w1, b, grp, g;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kFlashLowRegs));
+    griddep_wait_and_release();
+    if (warp == 0) {
+      // -------------------------------------------------------------- producer
+      run.start(tiles_of.items(), tiles_of.mult(), tiles_of, blockIdx.x, gridDim.x);
+      if (lane == 0) {
+        int st = 0;
+        uint32_t ph = 0, qph = 0, iss = 0, par = 0, qiss = 0, qpar = 0;
+        bool ok = true;
+        const uint32_t q_bytes = (uint32_t)(rs.rep * rs.qpt * 128 * C::CHUNKS);
+        while (ok && run.next(tiles_of, seg, w0, w1)) {
+          tiles_of.where(seg, b, grp, g);
+          for (int s = 0; s < C::NQ; ++s) {
+            const int rt = grp * C::NQ + s;
+            if (rt >= rs.tiles) break;
+            if (!mbar_wait(&bars.q_empty[s], ((qph >> s) & 1u) ^ 1u, wait_ns)) { ok = false; break; }
+            mbar_arrive_expect_tx(&bars.q_full[s], q_bytes);
+            for (int c = 0; c < C::CHUNKS; ++c)
+              tma_load_5d(smem + C::OFF_Q + s * C::Q_BYTES + c * C::TILE, &mapQ, &bars.q_full[s], c * 64, 0, g,
+                          rt * rs.qpt, b);
+            qiss |= 1u << s; qpar = (qpar & ~(1u << s)) | (qph & (1u << s));
+            qph ^= 1u << s;
+          }
+          if (!ok) break;
+          ok = rows_ring_order<PAIR>(w1 - w0, [&](bool is_v, int j) {
+            if (!mbar_wait(&bars.empty[st], ph ^ 1u, wait_ns)) return false;
+            mbar_arrive_expect_tx(&bars.full[st], C::KV_BYTES);
+            for (int c = 0; c < C::CHUNKS; ++c)
+              tma_load_4d(smem + C::OFF_RING + st * C::KV_BYTES + c * C::TILE, is_v ? &mapV : &mapK, &bars.full[st],
+                          c * 64, g, (w0 + j) * 128, b);
+            iss |= 1u << st; par = (par & ~(1u << st)) | (ph << st);
+            if (++st == C::RING) { st = 0; ph ^= 1u; }
+            return true;
+          });
+        }
+        for (int s = 0; s < 2; ++s)
+          if (qiss & (1u << s)) mbar_wait(&bars.q_full[s], (qpar >> s) & 1u, wait_ns);
+        for (int s = 0; s < C::RING; ++s)
+          if (iss & (1u << s)) mbar_wait(&bars.full[s], (par >> s) & 1u, wait_ns);
+      }
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- MMA issuer
+      constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t IDESC_O = idesc_bf16_f32(128, HD, 0, 1);   // A = P (TMEM), B = V MN-major
+      run.start(tiles_of.items(), tiles_of.mult(), tiles_of, blockIdx.x, gridDim.x);
+      const bool leader = elect_one_sync();
+      const uint32_t q_addr = smem_u32(smem + C::OFF_Q), ring_addr = smem_u32(smem + C::OFF_RING);
+      int st = 0;
+      uint32_t ph = 0, qph = 0, pph = 0;
+      bool ok = true;
+      // the next tile of the ring, once it has landed; -1 if the wait gave up
+      auto take = [&]() -> int {
+        if (!mbar_wait_warp(&bars.full[st], ph, wait_ns)) return -1;
+        const int got = st;
+        if (++st == C::RING) { st = 0; ph ^= 1u; }
+        tc_fence_after();
+        return got;
+      };
+      auto issue_s = [&](int s, int kst) {
+        const uint32_t qa = q_addr + (PAIR ? s * C::Q_BYTES : 0), ka = ring_addr + kst * C::KV_BYTES;
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k) {
+            const uint32_t off = (k >> 2) * C::TILE + (k & 3) * 32;
+            tc_mma_f16_ss(tmem_base + s * 256, sw128_desc(qa + off, 1024, 16), sw128_desc(ka + off, 1024, 16), IDESC_S,
+                          k > 0);
+          }
+          tc_commit(&bars.s_full[s]);
+        }
+        __syncwarp();
+      };
+      // waits for the halves of slot s's P and adds P V; false if a wait gave up
+      auto issue_pv = [&](int s, int vst, bool accumulate) -> bool {
+        const uint32_t va = ring_addr + vst * C::KV_BYTES;
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait_warp(half ? &bars.p_full[s] : &bars.p_half[s], (pph >> s) & 1u, wait_ns)) return false;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int kk = half * 4 + k;
+              tc_mma_f16_ts(tmem_base + s * 256 + 128, tmem_base + s * 256 + kk * 8,
+                            sw128_desc(va + kk * 2048, 1024, C::TILE), IDESC_O, (accumulate || kk > 0) ? 1u : 0u);
+            }
+            if (half) tc_commit(&bars.o_done[s]);
+          }
+          __syncwarp();
+        }
+        pph ^= 1u << s;
+        return true;
+      };
+      // V rows from `valid` on become zero
+      auto clear_tail = [&](int vst, int valid) {
+        uint8_t* v = smem + C::OFF_RING + vst * C::KV_BYTES;
+        for (int c = 0; c < C::CHUNKS; ++c)
+          for (int i = valid * 8 + lane; i < 128 * 8; i += 32)
+            *reinterpret_cast<uint4*>(v + c * C::TILE + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      while (ok && run.next(tiles_of, seg, w0, w1)) {
+        tiles_of.where(seg, b, grp, g);
+        const int n = w1 - w0;
+        const int held = cached_len(rs.kv_lens, b, rs.max_len) + (TREE ? 0 : cached_len(rs.seq_lens, b, rs.T));
+        const int nslots = PAIR ? (grp * 2 + 1 < rs.tiles ? 2 : 1) : 1;
+        for (int s = 0; s < nslots; ++s) {
+          if (!mbar_wait_warp(&bars.q_full[s], (qph >> s) & 1u, wait_ns)) ok = false;
+          qph ^= 1u << s;
+        }
+        if (!ok) break;
+        tc_fence_after();
+        // S of tile i for every slot that works on it; with !PAIR slot i & 1
+        auto scores = [&](int i) -> bool {
+          const int kst = take();
+          if (kst < 0) return false;
+          if (PAIR) {
+            for (int s = 0; s < nslots; ++s) issue_s(s, kst);
+          } else {
+            issue_s(i & 1, kst);
+          }
+          if (leader) tc_commit(&bars.empty[kst]);
+          __syncwarp();
+          return true;
+        };
+        ok = scores(0) && (PAIR || n < 2 || scores(1));
+        for (int j = 0; j < n && ok; ++j) {
+          const int vst = take();
+          if (vst < 0) { ok = false; break; }
+          if ((w0 + j) * 128 + 128 > held) clear_tail(vst, held - (w0 + j) * 128);
+          if (PAIR) {
+            int kst = -1;
+            for (int s = 0; s < nslots && ok; ++s) {
+              ok = issue_pv(s, vst, j > 0);
+              if (ok && j + 1 < n) {
+                if (s == 0) kst = take();
+                ok = kst >= 0;
+                if (ok) issue_s(s, kst);
+              }
+            }
+            if (!ok) break;
+            if (leader) {
+              tc_commit(&bars.empty[vst]);
+              if (kst >= 0) tc_commit(&bars.empty[kst]);
+            }
+            __syncwarp();
+          } else {
+            ok = issue_pv(j & 1, vst, j > 1);
+            if (!ok) break;
+            if (leader) tc_commit(&bars.empty[vst]);
+            __syncwarp();
+            if (j + 2 < n) ok = scores(j + 2);
+          }
+        }
+        if (leader)
+          for (int s = 0; s < nslots; ++s) tc_commit(&bars.q_empty[s]);
+        __syncwarp();
+      }
+    } else if (!TREE) {
+      // -------------------------------------------------------------- zeros for the padding rows
+      const int row16 = rs.H * HD * 2 / 16;
+      const int w = blockIdx.x * 2 + warp - 2;
+      for (int i = w; i < rs.B * rs.T; i += gridDim.x * 2) {
+        if (i % rs.T < cached_len(rs.seq_lens, i / rs.T, rs.T)) continue;
+        uint4* o = static_cast<uint4*>(rs.out) + (size_t)i * row16;
+        for (int k = lane; k < row16; k += 32) o[k] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kFlashHighRegs));
+    griddep_wait_and_release();
+    // ---------------------------------------------------------------- softmax (one thread per row)
+    const int slot = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;            // row of the tile == TMEM lane
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_tmem = tmem_base + lane_off + slot * 256;
+    const uint32_t o_tmem = s_tmem + 128;
+    const int t_in = row / rs.rep;                  // this row's position and head within the tile
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    uint32_t sph = 0, oph = 0, mph = 0;
+    bool merged = false;                            // a join is open: the other warpgroup may still read O
+    run.start(tiles_of.items(), tiles_of.mult(), tiles_of, blockIdx.x, gridDim.x);
+    while (run.next(tiles_of, seg, w0, w1)) {
+      tiles_of.where(seg, b, grp, g);
+      const int rt = PAIR ? grp * 2 + slot : grp;
+      if (PAIR && rt >= rs.tiles) continue;
+      const int len = cached_len(rs.kv_lens, b, rs.max_len);
+      const int t = rt * rs.qpt + t_in;
+      const int last = TREE ? len - 1 : len + t;                     // last key this row sees
+      const int last_min = TREE ? len - 1 : len + rt * rs.qpt;       // and the tile's first row
+      const int n = w1 - w0;
+      float m_ref = -INFINITY, l = 0.f;
+      bool ok = true, first = true;
+      for (int j = PAIR ? 0 : slot; j < n; j += PAIR ? 1 : 2) {
+        if (!mbar_wait_warp(&bars.s_full[slot], sph, wait_ns)) { ok = false; break; }
+        sph ^= 1u;
+        tc_fence_after();
+        const int key0 = (w0 + j) * 128;
+        const bool need_mask = key0 + 127 > last_min;
+        uint32_t ra[32], rb[32], rc[32], rd[32];
+        flash_load_row(s_tmem, ra, rb, rc, rd);
+        float m0, m1, m2, m3;
+        if (need_mask) {
+          m0 = flash_row_max<true>(ra, key0, last, 0);
+          m1 = flash_row_max<true>(rb, key0 + 32, last, 0);
+          m2 = flash_row_max<true>(rc, key0 + 64, last, 0);
+          m3 = flash_row_max<true>(rd, key0 + 96, last, 0);
+        } else {
+          m0 = flash_row_max<false>(ra, key0, last, 0);
+          m1 = flash_row_max<false>(rb, key0 + 32, last, 0);
+          m2 = flash_row_max<false>(rc, key0 + 64, last, 0);
+          m3 = flash_row_max<false>(rd, key0 + 96, last, 0);
+        }
+        const float m_tile = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * rs.scale_log2;
+        // the slot's previous P.V is complete: its S was issued behind it
+        if (!first) oph ^= 1u;
+        const bool grow = m_tile > m_ref + 8.0f;
+        float alpha = 1.f;
+        if (grow) {
+          alpha = exp2f(m_ref - m_tile);
+          l *= alpha;
+          m_ref = m_tile;
+        }
+        if (!first && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_tmem + c * 16, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st16(o_tmem + c * 16, o);
+          }
+          tc_wait_st();
+        }
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        float la, lb;
+        if (need_mask)
+          la = rows_exp_half<true, !TREE>(ra, rb, rs.scale_log2, neg_m, s_tmem);
+        else
+          la = rows_exp_half<false, !TREE>(ra, rb, rs.scale_log2, neg_m, s_tmem);
+        if (!PAIR && merged) {
+          // the first P.V of this piece overwrites O: the other warpgroup has to have read the last piece's
+          if (!mbar_wait_warp(&bars.merge[1], mph ^ 1u, wait_ns)) { ok = false; break; }
+          merged = false;
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars.p_half[slot]);
+        if (need_mask)
+          lb = rows_exp_half<true, !TREE>(rc, rd, rs.scale_log2, neg_m, s_tmem + 32);
+        else
+          lb = rows_exp_half<false, !TREE>(rc, rd, rs.scale_log2, neg_m, s_tmem + 32);
+        l += la + lb;
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars.p_full[slot]);
+        first = false;
+      }
+      if (!ok) break;
+      if (!first) {
+        if (!mbar_wait_warp(&bars.o_done[slot], oph, wait_ns)) break;
+        oph ^= 1u;
+        tc_fence_after();
+      }
+      // f_own, f_oth: this warpgroup's and the other one's share in the result
+      float m = m_ref, f_own = 1.f, f_oth = 0.f;
+      if (!PAIR) {
+        if (merged) {   // this warpgroup had no tile, so it has not waited yet
+          if (!mbar_wait_warp(&bars.merge[1], mph ^ 1u, wait_ns)) break;
+          merged = false;
+        }
+        ml[slot * 128 + row] = make_float2(m_ref, l);
+        tc_fence_before();
+        mbar_arrive(&bars.merge[0]);
+        if (!mbar_wait_warp(&bars.merge[0], mph, wait_ns)) break;
+        tc_fence_after();
+        const float2 oth = ml[(slot ^ 1) * 128 + row];
+        m = fmaxf(m_ref, oth.x);
+        f_own = m_ref == -INFINITY ? 0.f : exp2f(m_ref - m);
+        f_oth = oth.x == -INFINITY ? 0.f : exp2f(oth.x - m);
+        l = l * f_own + oth.y * f_oth;
+        mph ^= 1u;
+        merged = true;
+      }
+      const int live = TREE ? rs.T : cached_len(rs.seq_lens, b, rs.T);
+      const bool real = t_in < rs.qpt && t < live;
+      const bool whole = !TREE && w0 == 0 && w1 == seg.n;
+      const int R = PAIR ? 256 : 128, rrow = PAIR ? slot * 128 + row : row;
+      const size_t id = tiles_of.record(seg, blockIdx.x, run.a);
+      if ((PAIR || slot == 0) && real) {
+        if (whole)
+          rs.nlse[((size_t)(b * rs.KV + g) * rs.tiles + rt) * 128 + row] = -(m + log2f(l));
+        else
+          *reinterpret_cast<float2*>(rs.part_ml + (id * R + rrow) * 2) = make_float2(m, l);
+      }
+      const float inv = 1.f / l;
+      uint8_t* stage = smem + C::OFF_STAGE + (warp - 4) * 2048;
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        if (!PAIR && (c & 1) != slot) continue;    // the warpgroups share the columns
+        uint32_t r[32];
+        tmem_ld32(o_tmem + c * 32, r);
+        tc_wait_ld();
+        if (!PAIR) {
+          uint32_t q[32];
+          tmem_ld32((slot ? o_tmem - 256 : o_tmem + 256) + c * 32, q);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            // a warpgroup that saw no key has nothing in its O
+            const float own = f_own == 0.f ? 0.f : __uint_as_float(r[i]) * f_own;
+            r[i] = __float_as_uint(f_oth == 0.f ? own : fmaf(__uint_as_float(q[i]), f_oth, own));
+          }
+        }
+        if (whole) {
+          // as in flash_attention.cuh: through 2 KB of shared memory, 64 contiguous bytes per row
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint4 o;
+            o.x = pack_bf16x2(__uint_as_float(r[8 * k + 0]) * inv, __uint_as_float(r[8 * k + 1]) * inv);
+            o.y = pack_bf16x2(__uint_as_float(r[8 * k + 2]) * inv, __uint_as_float(r[8 * k + 3]) * inv);
+            o.z = pack_bf16x2(__uint_as_float(r[8 * k + 4]) * inv, __uint_as_float(r[8 * k + 5]) * inv);
+            o.w = pack_bf16x2(__uint_as_float(r[8 * k + 6]) * inv, __uint_as_float(r[8 * k + 7]) * inv);
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = o;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int mm = 0; mm < 4; ++mm) {
+            const int rr = mm * 8 + (lane >> 2), k = lane & 3;
+            const uint4 o = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((k ^ ((rr >> 1) & 3)) << 4));
+            const int tr = (quarter * 32 + rr) / rs.rep, jr = quarter * 32 + rr - tr * rs.rep;
+            if (tr < rs.qpt && rt * rs.qpt + tr < live)
+              *reinterpret_cast<uint4*>(static_cast<bf16*>(rs.out) +
+                                        (((size_t)b * rs.T + rt * rs.qpt + tr) * rs.H + g * rs.rep + jr) * HD +
+                                        c * 32 + k * 8) = o;
+          }
+          __syncwarp();
+        } else if (real) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(rs.part_o + ((id * (HD / 4) + c * 8 + k) * R + rrow) * 4) =
+                make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        }
+      }
+      tc_fence_before();
+      if (!PAIR) mbar_arrive(&bars.merge[1]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// ---- joining the pieces ------------------------------------------------------
+// A row's (m, l, acc): lane k holds dims 4k .. 4k+3 (k < HD / 4).
+struct RowAcc {
+  float m, l, a[4];
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.f;
+    a[0] = a[1] = a[2] = a[3] = 0.f;
+  }
+  // adds a piece; one that saw no key has nothing in its O
+  __device__ __forceinline__ void add(float pm, float pl, const float4& o) {
+    if (pm == -INFINITY) return;
+    const float mn = fmaxf(m, pm);
+    const float f = m == -INFINITY ? 0.f : exp2f(m - mn), fp = exp2f(pm - mn);
+    l = l * f + pl * fp;
+    a[0] = a[0] * f + o.x * fp;
+    a[1] = a[1] * f + o.y * fp;
+    a[2] = a[2] * f + o.z * fp;
+    a[3] = a[3] * f + o.w * fp;
+    m = mn;
+  }
+};
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const bf16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
+}
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(bf16* p, float a, float b, float c, float d) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
+
+// Adds the pieces of one row of segment seg to acc (whole warp); how many there were.
+template <int HD, bool TREE>
+__device__ __forceinline__ int join_pieces(const RowsShape& rs, const FlatSeg& seg, long long per, int rrow,
+                                           RowAcc& acc) {
+  const RowsTiles<TREE> tiles_of{rs};
+  const int lane = threadIdx.x & 31, R = rs.slots * rs.tile_rows;
+  int pieces = 0;
+  for (int c = (int)(seg.s0 / per); c <= (int)((seg.end() - 1) / per); ++c) {
+    int w0, w1;
+    if (!seg.cut(c * per, (c + 1) * per, w0, w1)) continue;
+    if (!TREE && w0 == 0 && w1 == seg.n) return 1;   // whole: written by its CTA, no record
+    const size_t id = tiles_of.record(seg, c, c * per);
+    const float2 ml = *reinterpret_cast<const float2*>(rs.part_ml + (id * R + rrow) * 2);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lane < HD / 4) o = load4(rs.part_o + ((id * (HD / 4) + lane) * R + rrow) * 4);
+    acc.add(ml.x, ml.y, o);
+    ++pieces;
+  }
+  return pieces;
+}
+
+// Tree attention, second half: a warp per row joins the pieces over the cache
+// with the node's own ancestors, whose keys it reads one by one -- a chain is
+// short next to the cache, and a product with the whole tree's values would
+// let the infinities of other nodes in (0 x inf).  The rows of 8 warps are
+// neighbours in (node, head), so their chains' rows come from L1.
+// blockIdx.x = (sequence, KV head), blockIdx.y = 8 rows.
+constexpr int kJoinWarps = 8;
+template <typename T, int HD>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    tree_join_kernel(const __grid_constant__ RowsShape rs, const T* __restrict__ q, const T* __restrict__ kn,
+                     const T* __restrict__ vn, const int32_t* __restrict__ parents) {
+  __shared__ int32_t par[kMaxTreeNodes];
+  __shared__ uint8_t chain_s[kJoinWarps][kMaxTreeNodes];
+  griddep_wait_and_release();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x / rs.KV, g = blockIdx.x % rs.KV;
+  for (int i = threadIdx.x; i < rs.T; i += blockDim.x) par[i] = parents[(size_t)b * rs.T + i];
+  __syncthreads();
+  const int r = blockIdx.y * kJoinWarps + warp;     // row t * rep + j
+  if (r >= rs.T * rs.rep) return;
+  const int t = r / rs.rep, h = g * rs.rep + r % rs.rep;
+  T* o = static_cast<T*>(rs.out) + (((size_t)b * rs.T + t) * rs.H + h) * HD;
+  const bool on = lane < HD / 4;
+  // the chain from the node up to its root
+  uint8_t* chain = chain_s[warp];
+  int depth = 0;
+  bool live = false;
+  for (int c = t;;) {
+    if (lane == 0) chain[depth] = (uint8_t)c;
+    ++depth;
+    const int p = par[c];
+    if (p >= c) record_error(LLAMA3_ERR_ARG);
+    if (p < 0 || p >= c) {
+      live = p == -1;
+      break;
+    }
+    c = p;
+  }
+  if (!live) {
+    if (on) store4(o + 4 * lane, 0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  __syncwarp();
+  RowAcc acc;
+  acc.clear();
+  const RowsTiles<true> tiles_of{rs};
+  FlatSeg seg;
+  seg.item = b;
+  seg.n = rs.G > 0 ? tiles_of(b) : 0;
+  if (seg.n > 0) {
+    const int mult = tiles_of.mult();
+    const long long per = (flat_total(rs.B, mult, tiles_of) + rs.G - 1) / rs.G;
+    long long before = 0;
+    for (int i = lane; i < b; i += 32) before += flat_cost(tiles_of(i));
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) before += __shfl_xor_sync(0xffffffffu, before, s);
+    const int rt = t / rs.qpt, grp = rt / rs.slots;
+    seg.sub = grp * rs.KV + g;
+    seg.s0 = before * mult + (long long)seg.sub * flat_cost(seg.n);
+    join_pieces<HD, true>(rs, seg, per, (rt - grp * rs.slots) * rs.tile_rows + r - rt * rs.qpt * rs.rep, acc);
+  }
+  float4 qv = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (on) qv = load4(q + (((size_t)b * rs.T + t) * rs.H + h) * HD + 4 * lane);
+  // four keys at a time, so that their loads and sums overlap
+  for (int i0 = 0; i0 < depth; i0 += 4) {
+    float sc[4];
+    float4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      sc[u] = 0.f;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + u < depth && on) {
+        const size_t at = (((size_t)b * rs.T + chain[i0 + u]) * rs.KV + g) * HD + 4 * lane;
+        const float4 k = load4(kn + at);
+        v[u] = load4(vn + at);
+        sc[u] = fmaf(qv.x, k.x, fmaf(qv.y, k.y, fmaf(qv.z, k.z, qv.w * k.w)));
+      }
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sc[u] += __shfl_xor_sync(0xffffffffu, sc[u], s);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u < depth) acc.add(sc[u] * rs.scale_log2, 1.f, v[u]);
+  }
+  const float inv = 1.f / acc.l;
+  if (on) store4(o + 4 * lane, acc.a[0] * inv, acc.a[1] * inv, acc.a[2] * inv, acc.a[3] * inv);
+}
+
+// Observed attention: the rows of the segments that were cut.  blockIdx.x + 1 is
+// the border between two CTAs' runs; the first border within a segment takes
+// it.  blockIdx.y = 64 rows.
+template <typename T, int HD>
+__global__ void __launch_bounds__(32 * kJoinWarps) causal_join_kernel(const __grid_constant__ RowsShape rs) {
+  griddep_wait_and_release();
+  const RowsTiles<false> tiles_of{rs};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long total = flat_total(tiles_of.items(), tiles_of.mult(), tiles_of);
+  const long long per = (total + rs.G - 1) / rs.G, pos = (blockIdx.x + 1) * per;
+  if (pos >= total) return;
+  const FlatSeg seg = flat_seek(tiles_of.items(), tiles_of.mult(), tiles_of, pos);
+  if (seg.s0 == pos || seg.s0 < pos - per) return;
+  int b, grp, g;
+  tiles_of.where(seg, b, grp, g);
+  const int live = cached_len(rs.seq_lens, b, rs.T);
+  const int first = blockIdx.y * 64 + warp, end = min(blockIdx.y * 64 + 64, rs.slots * rs.tile_rows);
+  for (int r = first; r < end; r += kJoinWarps) {
+    const int rt = grp * rs.slots + r / rs.tile_rows, in = r % rs.tile_rows;
+    const int t_in = in / rs.rep, t = rt * rs.qpt + t_in, h = g * rs.rep + in - t_in * rs.rep;
+    if (t_in >= rs.qpt || t >= live) continue;
+    RowAcc acc;
+    acc.clear();
+    if (join_pieces<HD, false>(rs, seg, per, r, acc) < 2) continue;
+    const float inv = 1.f / acc.l;
+    if (lane < HD / 4)
+      store4(static_cast<T*>(rs.out) + (((size_t)b * rs.T + t) * rs.H + h) * HD + 4 * lane, acc.a[0] * inv,
+             acc.a[1] * inv, acc.a[2] * inv, acc.a[3] * inv);
+    if (lane == 0)
+      rs.nlse[((size_t)(b * rs.KV + g) * rs.tiles + rt) * rs.tile_rows + in] = -(acc.m + log2f(acc.l));
+  }
+}
+
+}  // namespace l3
