@@ -20,7 +20,9 @@ bool rows_supported(const llama3_config* c) { return rows_on_tc(c) || c->n_heads
 struct RowsPlan {
   RowsShape rs;
   bool tc, pair;
-  size_t ml, o, nlse, sums, total;
+  bool fits;       // the plans' units stay below 2^30
+  size_t ml, o, nlse, sums, scores, total;
+  bool scored;     // observed: the weights come from kept scores
 };
 RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len) {
   RowsPlan p;
@@ -41,6 +43,9 @@ RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len)
   const long long keys = (long long)max_len + (tree ? 0 : T);
   const long long work = (long long)B * rs.groups * rs.KV * ((keys + (1 << rs.key_shift) - 1) >> rs.key_shift);
   rs.G = (int)std::min((long long)num_sms() * (p.tc ? 1 : 2), work);
+  const long long units = (long long)B * rs.KV * rs.groups * (((keys + 63) >> rs.key_shift) + kFlatLead + 1);
+  const long long sums = tree ? 0 : (long long)B * rs.KV * ((keys >> (p.tc ? 8 : 6)) + 1) * (rs.tiles + kFlatLead);
+  p.fits = units < (1LL << 30) && sums < (1LL << 30);
   const size_t records = tree ? (size_t)B * rs.groups * rs.KV + rs.G : (size_t)2 * rs.G;
   const size_t rows = records * rs.slots * rs.tile_rows;
   size_t off = 0;
@@ -48,7 +53,12 @@ RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len)
   p.o = off; off += up256(rows * c->head_dim * 4);
   if (!tree) {
     p.nlse = off; off += up256((size_t)B * rs.KV * rs.tiles * rs.tile_rows * 4);
-    p.sums = off; off += up256((size_t)2 * num_sms() * 2 * rs.tile_rows * 4);
+    p.sums = off; off += up256((size_t)2 * num_sms() * 2 * 256 * 4);
+    // Scores kept in fp32 cost 8 bytes per row and slot (written, read), a second
+    // pass over K 2 hd bytes per slot: up to hd / 4 rows the scores are less.
+    p.scored = p.tc && (long long)T * rs.rep <= c->head_dim / 4 && (long long)B * rs.KV <= 65535;
+    p.scores = off;
+    if (p.scored) off += up256((size_t)B * rs.H * T * (((size_t)keys + 127) / 128 * 128) * 4);
   }
   p.total = rs.G > 0 ? off : 0;
   return p;
@@ -172,6 +182,7 @@ int run_observe(const llama3_config* c, RowsPlan& p, const ObserveArgs& a, cudaS
   rs.part_ml = ws_at<float>(a.ws, p.ml);
   rs.part_o = ws_at<float>(a.ws, p.o);
   rs.nlse = ws_at<float>(a.ws, p.nlse);
+  rs.scores = p.scored ? ws_at<float>(a.ws, p.scores) : nullptr;
   L3_TRY((run_rows<T, HD, false>(c, p, a.q, a.kc, a.vc, a.cap, st)));
   if (rs.G > 1) {
     L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
@@ -182,12 +193,18 @@ int run_observe(const llama3_config* c, RowsPlan& p, const ObserveArgs& a, cudaS
   WeightShape w;
   memset(&w, 0, sizeof(w));
   w.B = rs.B; w.S = rs.T; w.KV = rs.KV; w.rep = rs.rep; w.qpt = rs.qpt; w.tiles = rs.tiles; w.tile_rows = rs.tile_rows;
-  w.key_shift = rs.key_shift;
+  w.key_shift = p.tc ? 8 : 6;
   w.key_tiles = (rs.max_len + rs.T + (1 << w.key_shift) - 1) >> w.key_shift;
   w.max_len = rs.max_len; w.cap = a.cap; w.scale_log2 = rs.scale_log2;
   w.kv_lens = a.kv_lens; w.seq_lens = a.seq_lens; w.positions = a.positions;
   w.nlse = rs.nlse; w.win = a.win; w.wout = a.wout; w.slot_pos = a.slot_pos;
   w.part = ws_at<float>(a.ws, p.sums);
+  w.scores = rs.scores;
+  if (p.scored) {
+    L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
+              launch_k(scored_weights_kernel, dim3((rs.max_len + rs.T + 255) / 256, rs.B * rs.KV), 256, 0, st, w));
+    return launch_check();
+  }
   const long long most = (long long)w.B * w.key_tiles * w.KV * w.tiles;
   w.G = (int)std::min((long long)num_sms() * (p.tc ? 1 : 2), most);
   bool launched = false;
@@ -215,7 +232,7 @@ int run_observe(const llama3_config* c, RowsPlan& p, const ObserveArgs& a, cudaS
     L3_TRY(launch_check());
   }
   L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
-            launch_k(slot_weights_join_kernel, w.G - 1 + w.B, 128, 0, st, w));
+            launch_k(slot_weights_join_kernel, w.G - 1 + w.B, 256, 0, st, w));
   return launch_check();
 }
 
@@ -263,7 +280,9 @@ extern "C" {
 int llama3_tree_workspace_size(const llama3_config* cfg, int batch, int n_nodes, int max_len, size_t* bytes) {
   L3_TRY(check_tree_shape(cfg, batch, n_nodes, max_len));
   if (!bytes) return LLAMA3_ERR_ARG;
-  *bytes = plan_rows(cfg, true, batch, n_nodes, max_len).total;
+  const RowsPlan p = plan_rows(cfg, true, batch, n_nodes, max_len);
+  if (!p.fits) return LLAMA3_ERR_UNSUPPORTED;
+  *bytes = p.total;
   return LLAMA3_OK;
 }
 
@@ -278,6 +297,7 @@ int llama3_attention_tree(const llama3_config* cfg, const void* q, const void* k
       !aligned16(out) || !aligned4(kv_lens) || !aligned4(parents))
     return LLAMA3_ERR_ALIGN;
   RowsPlan p = plan_rows(cfg, true, batch, n_nodes, max_len);
+  if (!p.fits) return LLAMA3_ERR_UNSUPPORTED;
   if (p.total && (!ws || ws_bytes < p.total)) return LLAMA3_ERR_WORKSPACE;
   if (!aligned16(ws)) return LLAMA3_ERR_ALIGN;
   const TreeArgs a = {q, k_cache, v_cache, k_nodes, v_nodes, kv_lens, parents, cache_cap, out, ws};
@@ -290,7 +310,9 @@ int llama3_attention_tree(const llama3_config* cfg, const void* q, const void* k
 int llama3_observe_workspace_size(const llama3_config* cfg, int batch, int seq, int max_len, size_t* bytes) {
   L3_TRY(check_observe_shape(cfg, batch, seq, max_len));
   if (!bytes) return LLAMA3_ERR_ARG;
-  *bytes = plan_rows(cfg, false, batch, seq, max_len).total;
+  const RowsPlan p = plan_rows(cfg, false, batch, seq, max_len);
+  if (!p.fits) return LLAMA3_ERR_UNSUPPORTED;
+  *bytes = p.total;
   return LLAMA3_OK;
 }
 
@@ -307,6 +329,7 @@ int llama3_attention_observed(const llama3_config* cfg, const void* q, const voi
       !aligned4(slot_pos))
     return LLAMA3_ERR_ALIGN;
   RowsPlan p = plan_rows(cfg, false, batch, seq, max_len);
+  if (!p.fits) return LLAMA3_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < p.total) return LLAMA3_ERR_WORKSPACE;
   if (!aligned16(ws)) return LLAMA3_ERR_ALIGN;
   const ObserveArgs a = {q,          k_cache, v_cache,  kv_lens,   seq_lens, positions,
@@ -351,7 +374,10 @@ int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src
   L3_TRY(llama3_evict_workspace_size(cfg, n_layers, batch, max_len, budget, &need));
   if (!ws || ws_bytes < need) return LLAMA3_ERR_WORKSPACE;
   if (!aligned16(ws)) return LLAMA3_ERR_ALIGN;
-  if ((long long)std::min(n_layers, kEvictLayers) * batch * cfg->n_kv_heads > INT_MAX) return LLAMA3_ERR_ARG;
+  // the kernels count rows of one launch, and 16-byte pieces of one row, in 32 bits
+  if ((long long)std::min(n_layers, kEvictLayers) * batch * cfg->n_kv_heads > INT_MAX ||
+      (long long)std::min(max_len, budget) * 32 > INT_MAX / 2)
+    return LLAMA3_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const long long words = evict_row_words(max_len, budget);
   EvictParams p;
@@ -361,7 +387,15 @@ int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src
   p.B = batch; p.KV = cfg->n_kv_heads; p.row16 = (int)(cfg->head_dim * esize(cfg) / 16);
   p.cap = src_cap; p.dst_cap = dst ? dst_cap : src_cap;
   p.max_len = max_len; p.budget = budget; p.recent = recent; p.in_place = dst ? 0 : 1;
+  p.from_words = evict_kept(max_len, budget);
+  p.move_words = evict_moves(max_len, budget);
   p.ws_row = words;
+  // as many threads as a row has slots to look at, up to 512
+  const int threads = std::max(64, std::min(512, (max_len / 4 + 31) / 32 * 32));
+  const bool stored = max_len <= kEvictKeys;
+  const int smem = stored ? max_len * 4 : 0;
+  static bool done[kMaxDevices];
+  L3_TRY(opt_in_smem(evict_select_kernel<true>, kEvictKeys * 4, done));
   for (int l0 = 0; l0 < n_layers; l0 += kEvictLayers) {
     const int nl = std::min(kEvictLayers, n_layers - l0);
     for (int i = 0; i < nl; ++i) {
@@ -372,17 +406,17 @@ int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src
     }
     p.ws = (int32_t*)ws + (size_t)l0 * batch * cfg->n_kv_heads * words;
     const int rows = nl * batch * cfg->n_kv_heads;
-    L3_LAUNCH(LLAMA3_KERNEL_EVICT, st, launch_k(evict_select_kernel, rows, kEvictThreads, 0, st, p));
+    p.lens_out = l0 + nl == n_layers ? kv_lens_out : nullptr;
+    L3_LAUNCH(LLAMA3_KERNEL_EVICT, st,
+              launch_k(stored ? evict_select_kernel<true> : evict_select_kernel<false>, rows, threads, smem, st, p));
     L3_TRY(launch_check());
-    const long long pieces = (long long)std::min(max_len, budget) * p.row16;
-    const int parts = (int)std::max(1LL, std::min((pieces + 2047) / 2048, 64LL));
+    // parts of a row: enough blocks to fill the GPU, of at least four pieces per thread
+    const long long pieces = (long long)p.from_words * p.row16;
+    const int parts = (int)std::max(1LL, std::min((pieces + 1023) / 1024, 64LL));
     L3_LAUNCH(LLAMA3_KERNEL_EVICT, st, launch_k(evict_move_kernel, dim3(rows, parts), 256, 0, st, p));
     L3_TRY(launch_check());
   }
-  L3_LAUNCH(LLAMA3_KERNEL_EVICT, st,
-            launch_k(evict_lens_kernel, blocks_for(batch, 256), 256, 0, st, kv_lens, kv_lens_out, batch, max_len,
-                     budget));
-  return launch_check();
+  return LLAMA3_OK;
 }
 
 int llama3_tree_accept(const int32_t* draft_ids, const int32_t* target_ids, const int32_t* parents, int batch,

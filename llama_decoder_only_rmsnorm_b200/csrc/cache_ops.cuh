@@ -1,15 +1,11 @@
-// cache_ops.cuh -- operators around the K/V cache for drafted (speculative)
-// and bounded decoding, in their plain CUDA-core form: any head size, fp32 and
-// bf16.  Sums, softmax statistics and accumulated weights are fp32.
+// cache_ops.cuh -- operators on the rows of the K/V cache for drafted
+// (speculative) and bounded decoding; they move rows and decide which, and
+// compute nothing on them.
 //
-//   tree attention      node t of a drafted tree sees the cached rows
-//                       0..kv_len-1, its ancestors in the tree and itself
-//   observed attention  causal attention that also adds up, per cache slot and
-//                       KV head, the softmax weight the slot received
-//   eviction            the kept slots of a bounded cache, selected by
-//                       recency and accumulated weight
-//   acceptance          the path of the tree that the target's tokens confirm,
-//                       and the copy of its rows into the caches
+//   eviction    the kept slots of a bounded cache, selected by recency and
+//               accumulated weight
+//   acceptance  the path of a drafted tree that the target's tokens confirm,
+//               and the copy of its rows into the caches
 #pragma once
 #include <limits.h>
 
@@ -41,16 +37,20 @@ constexpr int kEvictLayers = 32;   // layers of one launch (the structs travel a
 struct EvictParams {
   EvictLayer layer[kEvictLayers];
   const int32_t *kv_lens, *positions;
-  int32_t* ws;
+  int32_t *ws, *lens_out;
   int B, KV, row16, cap, dst_cap, max_len, budget, recent, in_place;
-  long long ws_row;    // words of scratch per row (evict_row_words)
+  int from_words, move_words;
+  long long ws_row;    // words of scratch per row: 4, the sources, the holes and the slots that fill them
 };
 
-// Words of scratch per (layer, sequence, KV head): the number of moves, the
-// holes below the budget, and where each kept slot comes from.
-__host__ __device__ inline long long evict_row_words(int max_len, int budget) {
-  const long long moves = budget < max_len - budget ? budget : (max_len > budget ? max_len - budget : 0);
-  return 4 + moves + budget;
+// Kept slots of a row at most, and moves of one at most.
+inline int evict_kept(int max_len, int budget) { return budget < max_len ? budget : max_len; }
+inline int evict_moves(int max_len, int budget) {
+  const int out = max_len > budget ? max_len - budget : 0;
+  return out < budget ? out : budget;
+}
+inline long long evict_row_words(int max_len, int budget) {
+  return 4LL + evict_kept(max_len, budget) + 2LL * evict_moves(max_len, budget);
 }
 
 // Order key of a slot: larger is kept first.  Recent slots come before all
@@ -61,33 +61,44 @@ __device__ __forceinline__ uint32_t evict_key(float w, int32_t pos, long long fl
   return float_order_key(w == 0.f ? 0.f : w);
 }
 
-// Exclusive prefix sum over a block of 1024 threads of a 0/1 flag; total to all.
-__device__ __forceinline__ int block_rank(bool f, int* warp_tot, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t m = __ballot_sync(0xffffffffu, f);
-  __syncthreads();
-  if (lane == 0) warp_tot[warp] = __popc(m);
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < 32; ++i) {
-    const int c = warp_tot[i];
-    before += i < warp ? c : 0;
-    all += c;
+// Exclusive prefix sums over the block of two counts at once; totals to all.
+// s: 2 * 32 ints.  Every thread of the block.
+__device__ __forceinline__ void block_scan2(int& x, int& y, int& tx, int& ty, int* s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int ix = x, iy = y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int ux = __shfl_up_sync(0xffffffffu, ix, o), uy = __shfl_up_sync(0xffffffffu, iy, o);
+    if (lane >= o) { ix += ux; iy += uy; }
   }
-  total = all;
-  return before + __popc(m & ((1u << lane) - 1u));
+  __syncthreads();
+  if (lane == 31) { s[warp] = ix; s[32 + warp] = iy; }
+  __syncthreads();
+  const int wx = lane < warps ? s[lane] : 0, wy = lane < warps ? s[32 + lane] : 0;
+  x = ix - x + __reduce_add_sync(0xffffffffu, lane < warp ? wx : 0);
+  y = iy - y + __reduce_add_sync(0xffffffffu, lane < warp ? wy : 0);
+  tx = __reduce_add_sync(0xffffffffu, wx);
+  ty = __reduce_add_sync(0xffffffffu, wy);
 }
 
-constexpr int kEvictThreads = 1024;
+// Order keys of a row that a block keeps in shared memory (128 KB); longer rows
+// compute them anew at every look.
+constexpr int kEvictKeys = 32768;
 
-// One block per (layer, sequence, KV head): the budget-th largest key by four
-// passes of an 8-bit radix select, then the kept slots in order.
-__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+// One block per (layer, sequence, KV head).  Thread i owns the slots [i * per, (i +
+// 1) * per), so ranks by slot are prefix sums over the threads.  The cut -- the
+// budget-th largest key -- is found two bits at a time by counting: three
+// thresholds per look, counts added up by redux and once through shared
+// memory.  (A radix histogram has most of its increments on a few bins here,
+// since the weights share their exponents: @RADIX@ us against @COUNT@ us for 512 rows
+// of 8192 slots.)  A look whose count is the budget itself ends the search.
+template <bool STORED>
+__global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ uint32_t evict_keys[];
+  __shared__ int scan[64], counts[2][3][16];
   griddep_wait_and_release();
-  __shared__ int hist[256], warp_tot[32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
   const int row = blockIdx.x, g = row % p.KV, b = (row / p.KV) % p.B, layer = row / (p.KV * p.B);
+  const int NT = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = NT >> 5;
   const int n = cached_len(p.kv_lens, b, p.max_len), left = min(n, p.budget);
   const size_t base = ((size_t)b * p.KV + g) * p.cap;
   const float* w = p.layer[layer].w + base;
@@ -95,83 +106,131 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
   const long long floor_pos = (long long)p.positions[b] - p.recent;
   int32_t* ws = p.ws + (size_t)row * p.ws_row;
   int32_t* from = ws + 4;                  // source of every kept slot
-  int32_t* holes = ws + 4 + p.budget;
+  int32_t* holes = ws + 4 + p.from_words;
   if (n <= p.budget) {
     if (threadIdx.x == 0) ws[0] = 0;
-    for (int i = threadIdx.x; i < left; i += kEvictThreads) from[i] = i;
+    for (int i = threadIdx.x; i < left; i += NT) from[i] = i;
     return;
   }
-  if (threadIdx.x == 0) { s_prefix = 0; s_need = p.budget; }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-    __syncthreads();
-    const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int j = threadIdx.x; j < n; j += kEvictThreads) {
-      const uint32_t key = evict_key(w[j], pos[j], floor_pos);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int need = s_need, d = 255;
-      while (d > 0 && hist[d] < need) need -= hist[d--];
-      s_prefix = prefix | ((uint32_t)d << shift);
-      s_need = need;
-    }
+  if (STORED) {
+    for (int j = threadIdx.x; j < n; j += NT) evict_keys[j] = evict_key(w[j], pos[j], floor_pos);
     __syncthreads();
   }
-  const uint32_t cut = s_prefix;
-  const int ties = s_need;     // slots at the cut that are kept: the lowest ones
-  int seen_ties = 0, n_holes = 0, n_fill = 0;
-  for (int j0 = 0; j0 < n; j0 += kEvictThreads) {
-    const int j = j0 + threadIdx.x;
-    const bool in = j < n;
-    const uint32_t key = in ? evict_key(w[j], pos[j], floor_pos) : 0u;
-    int tot;
-    const int rank = seen_ties + block_rank(in && key == cut, warp_tot, tot);
-    seen_ties += tot;
-    const bool keep = in && (key > cut || (key == cut && rank < ties));
-    const bool hole = in && j < p.budget && !keep, fill = keep && j >= p.budget;
-    const int hr = n_holes + block_rank(hole, warp_tot, tot);
-    n_holes += tot;
-    const int fr = n_fill + block_rank(fill, warp_tot, tot);
-    n_fill += tot;
-    if (in && j < p.budget && keep) from[j] = j;
-    if (hole) holes[hr] = j;
-    __syncthreads();          // the r-th kept slot behind the budget fills the r-th hole
-    if (fill) from[holes[fr]] = j;
+  // an odd stride: 32 threads at the same place of their runs read 32 banks
+  const int per = ((n + NT - 1) / NT) | 1;
+  const int j0 = min(n, (int)threadIdx.x * per), j1 = min(n, j0 + per);
+  auto key_at = [&](int j) { return STORED ? evict_keys[j] : evict_key(w[j], pos[j], floor_pos); };
+  uint32_t cut = 0;      // at least `budget` keys are >= cut
+  for (int shift = 30, look = 0; shift >= 0; shift -= 2, look ^= 1) {
+    const uint32_t t1 = cut | (1u << shift), t2 = cut | (2u << shift), t3 = cut | (3u << shift);
+    int c1 = 0, c2 = 0, c3 = 0;
+    for (int j = j0; j < j1; ++j) {
+      const uint32_t k = key_at(j);
+      c1 += k >= t1;
+      c2 += k >= t2;
+      c3 += k >= t3;
+    }
+    c1 = __reduce_add_sync(0xffffffffu, c1);
+    c2 = __reduce_add_sync(0xffffffffu, c2);
+    c3 = __reduce_add_sync(0xffffffffu, c3);
+    if (lane == 0) { counts[look][0][warp] = c1; counts[look][1][warp] = c2; counts[look][2][warp] = c3; }
+    __syncthreads();     // the next look but one writes here again, behind the next look's barrier
+    c1 = __reduce_add_sync(0xffffffffu, lane < warps ? counts[look][0][lane] : 0);
+    c2 = __reduce_add_sync(0xffffffffu, lane < warps ? counts[look][1][lane] : 0);
+    c3 = __reduce_add_sync(0xffffffffu, lane < warps ? counts[look][2][lane] : 0);
+    int found = 0;
+    if (c3 >= p.budget) { cut = t3; found = c3; }
+    else if (c2 >= p.budget) { cut = t2; found = c2; }
+    else if (c1 >= p.budget) { cut = t1; found = c1; }
+    if (found == p.budget) break;
   }
-  if (threadIdx.x == 0) ws[0] = n_holes;
+  // of the slots at the cut the lowest are kept, as many as the budget leaves
+  int above = 0, equal = 0, all_above, all_equal;
+  for (int j = j0; j < j1; ++j) {
+    const uint32_t k = key_at(j);
+    above += k > cut;
+    equal += k == cut;
+  }
+  const int my_equal = equal;
+  block_scan2(above, equal, all_above, all_equal, scan);
+  const int room = p.budget - all_above;       // for keys equal to the cut
+  int taken = min(max(room - equal, 0), my_equal);
+  // the evicted slots below the budget and the kept ones behind it
+  int n_holes = 0, n_spare = 0, all_holes, all_spare;
+  {
+    int eq = taken;
+    for (int j = j0; j < j1; ++j) {
+      const uint32_t k = key_at(j);
+      const bool keep = k > cut || (k == cut && eq-- > 0);
+      n_holes += j < p.budget && !keep;
+      n_spare += j >= p.budget && keep;
+    }
+  }
+  block_scan2(n_holes, n_spare, all_holes, all_spare, scan);
+  int32_t* spare = holes + p.move_words;
+  for (int j = j0; j < j1; ++j) {
+    const uint32_t k = key_at(j);
+    const bool keep = k > cut || (k == cut && taken-- > 0);
+    if (j < p.budget) {
+      if (keep) from[j] = j; else holes[n_holes++] = j;
+    } else if (keep) {
+      spare[n_spare++] = j;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < all_holes; i += NT) from[holes[i]] = spare[i];
+  if (threadIdx.x == 0) ws[0] = all_holes;
 }
 
 // Copies the kept slots: blockIdx.x = row, blockIdx.y = part of the row's slots.
+// Four 16-byte pieces of K and of V in flight per thread.  The last launch of a
+// call also writes the lengths: kv_lens_out may be kv_lens, whose shortened
+// values give every block here the same `left`.
 __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictParams p) {
   griddep_wait_and_release();
   const int row = blockIdx.x, g = row % p.KV, b = (row / p.KV) % p.B, layer = row / (p.KV * p.B);
   const EvictLayer& L = p.layer[layer];
   const int left = min(cached_len(p.kv_lens, b, p.max_len), p.budget);
+  if (p.lens_out && row == b * p.KV && blockIdx.y == 0 && threadIdx.x == 0) p.lens_out[b] = left;
   const int32_t* ws = p.ws + (size_t)row * p.ws_row;
   const int32_t* from = ws + 4;
-  const int32_t* holes = ws + 4 + p.budget;
+  const int32_t* holes = ws + 4 + p.from_words;
   const int moves = p.in_place ? ws[0] : left;
   const size_t sbase = ((size_t)b * p.KV + g) * p.cap, dbase = ((size_t)b * p.KV + g) * p.dst_cap;
-  for (long long i = (long long)blockIdx.y * 256 + threadIdx.x; i < (long long)moves * p.row16; i += 256LL * gridDim.y) {
-    const int m = (int)(i / p.row16), c = (int)(i % p.row16);
-    const int to = p.in_place ? holes[m] : m, fr = from[to];
-    const size_t s = (((size_t)b * p.cap + fr) * p.KV + g) * p.row16 + c;
-    const size_t d = (((size_t)b * p.dst_cap + to) * p.KV + g) * p.row16 + c;
-    L.dk[d] = L.k[s];
-    L.dv[d] = L.v[s];
-    if (c == 0) {
-      L.dw[dbase + to] = L.w[sbase + fr];
-      L.dpos[dbase + to] = L.pos[sbase + fr];
+  const int total = moves * p.row16, step = 256 * gridDim.y;
+  for (int i0 = blockIdx.y * 256 + threadIdx.x; i0 < total; i0 += 4 * step) {
+    uint4 k[4], v[4];
+    int to[4], fr[4], c[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * step;
+      to[u] = -1;
+      if (i < total) {
+        const int m = i / p.row16;
+        c[u] = i - m * p.row16;
+        to[u] = p.in_place ? holes[m] : m;
+        fr[u] = from[to[u]];
+      }
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (to[u] >= 0) {
+        const size_t at = (((size_t)b * p.cap + fr[u]) * p.KV + g) * p.row16 + c[u];
+        k[u] = L.k[at];
+        v[u] = L.v[at];
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (to[u] >= 0) {
+        const size_t at = (((size_t)b * p.dst_cap + to[u]) * p.KV + g) * p.row16 + c[u];
+        L.dk[at] = k[u];
+        L.dv[at] = v[u];
+        if (c[u] == 0) {
+          L.dw[dbase + to[u]] = L.w[sbase + fr[u]];
+          L.dpos[dbase + to[u]] = L.pos[sbase + fr[u]];
+        }
+      }
   }
-}
-
-__global__ void evict_lens_kernel(const int32_t* kv_lens, int32_t* lens_out, int B, int max_len, int budget) {
-  griddep_wait_and_release();
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b < B) lens_out[b] = min(cached_len(kv_lens, b, max_len), budget);
 }
 
 // ---- acceptance -------------------------------------------------------------

@@ -9,6 +9,7 @@
 // that crosses a border is cut into pieces there.  Every warp derives the plan
 // from the lengths alone, in the same way, so nothing is communicated.
 //
+// Units are counted in 32 bits; the host refuses work beyond 2^30 of them.
 // Items are what has a length (a sequence, or a sequence's query block); each
 // item stands for `mult` segments of the same n.  NOf is a functor int(int item).
 #pragma once
@@ -24,42 +25,40 @@ __device__ __forceinline__ int flat_cost(int n) { return n > 0 ? n + kFlatLead :
 
 // Cost of all items; every lane gets it.  Whole warp.
 template <class NOf>
-__device__ __forceinline__ long long flat_total(int items, int mult, const NOf& n_of) {
-  long long t = 0;
+__device__ __forceinline__ int flat_total(int items, int mult, const NOf& n_of) {
+  int t = 0;
   for (int i = threadIdx.x & 31; i < items; i += 32) t += flat_cost(n_of(i));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  return t * mult;
+  return __reduce_add_sync(0xffffffffu, t) * mult;
 }
 
 // One segment: segment `sub` of `item`, n tiles, at cost units s0 .. s0 + n + kFlatLead - 1.
 struct FlatSeg {
   int item, sub, n;
-  long long s0;
-  __device__ __forceinline__ long long end() const { return s0 + n + kFlatLead; }
+  int s0;
+  __device__ __forceinline__ int end() const { return s0 + n + kFlatLead; }
   // The tiles [w0, w1) of this segment within the units [a, e); false if there are none.
-  __device__ __forceinline__ bool cut(long long a, long long e, int& w0, int& w1) const {
-    w0 = (int)max(0LL, a - s0 - kFlatLead);
-    w1 = (int)(min(e, end()) - s0) - kFlatLead;
+  __device__ __forceinline__ bool cut(int a, int e, int& w0, int& w1) const {
+    w0 = max(0, a - s0 - kFlatLead);
+    w1 = min(e, end()) - s0 - kFlatLead;
     return w1 > w0;
   }
 };
 
 // The segment that unit `pos` (< total) lies in.  Whole warp.
 template <class NOf>
-__device__ __forceinline__ FlatSeg flat_seek(int items, int mult, const NOf& n_of, long long pos) {
+__device__ __forceinline__ FlatSeg flat_seek(int items, int mult, const NOf& n_of, int pos) {
   const int lane = threadIdx.x & 31;
-  long long base = 0;
+  int base = 0;
   FlatSeg s;
   s.item = s.sub = s.n = 0;
   s.s0 = 0;
   for (int i0 = 0; i0 < items; i0 += 32) {
     const int n = i0 + lane < items ? n_of(i0 + lane) : 0;
-    const long long own = (long long)flat_cost(n) * mult;
-    long long incl = own;
+    const int own = flat_cost(n) * mult;
+    int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
     const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > pos);
@@ -67,9 +66,9 @@ __device__ __forceinline__ FlatSeg flat_seek(int items, int mult, const NOf& n_o
       const int l = __ffs(hit) - 1;
       s.item = i0 + l;
       s.n = __shfl_sync(0xffffffffu, n, l);
-      const long long start = base + __shfl_sync(0xffffffffu, incl - own, l);
-      s.sub = (int)((pos - start) / flat_cost(s.n));
-      s.s0 = start + (long long)s.sub * flat_cost(s.n);
+      const int start = base + __shfl_sync(0xffffffffu, incl - own, l);
+      s.sub = (pos - start) / flat_cost(s.n);
+      s.s0 = start + s.sub * flat_cost(s.n);
       return s;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -81,15 +80,15 @@ __device__ __forceinline__ FlatSeg flat_seek(int items, int mult, const NOf& n_o
 template <class NOf>
 struct FlatRun {
   FlatSeg seg;
-  long long a, e;
+  int a, e;
   int items, mult;
   bool more;
   // Whole warp.
   __device__ __forceinline__ void start(int items_, int mult_, const NOf& n_of, int c, int G) {
     items = items_;
     mult = mult_;
-    const long long total = flat_total(items, mult, n_of);
-    const long long per = (total + G - 1) / G;
+    const int total = flat_total(items, mult, n_of);
+    const int per = (total + G - 1) / G;
     a = per * c;
     e = min(a + per, total);
     more = a < e;

@@ -41,6 +41,7 @@ struct RowsShape {
   float scale_log2;                  // log2(e) / sqrt(hd)
   const int32_t *kv_lens, *seq_lens;
   float *part_ml, *part_o;           // records: [id][row][2] and [id][hd/4][row][4], slots * tile_rows rows
+  float* scores;                     // observed, few rows: [B][H * T][key tiles * 128] in the log2 domain, or NULL
   float* nlse;                       // observed: minus the rows' log-sum-exp (log2), [B * KV][tiles][tile_rows]
   void* out;
 };
@@ -68,7 +69,7 @@ struct RowsTiles {
   // works on.  Tree: every piece has one, and the segment's number plus the
   // CTA's is another for each.  Causal: only the pieces of cut segments, which
   // lie at the ends of a CTA's run.
-  __device__ __forceinline__ int record(const FlatSeg& s, int c, long long a) const {
+  __device__ __forceinline__ int record(const FlatSeg& s, int c, int a) const {
     return TREE ? s.item * mult() + s.sub + c : 2 * c + (s.s0 < a ? 0 : 1);
   }
 };
@@ -141,6 +142,13 @@ __device__ __forceinline__ float rows_exp_half(uint32_t (&ra)[32], uint32_t (&rb
   flash_pack_store(ra, taddr);
   flash_pack_store(rb, taddr + 16);
   return (s0 + s1) + (s2 + s3);
+}
+
+__device__ __forceinline__ void rows_put_scores(const uint32_t (&r)[32], float* s, float scl) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4)
+    *reinterpret_cast<float4*>(s + i) = make_float4(__uint_as_float(r[i]) * scl, __uint_as_float(r[i + 1]) * scl,
+                                                    __uint_as_float(r[i + 2]) * scl, __uint_as_float(r[i + 3]) * scl);
 }
 
 struct RowsBars {
@@ -388,6 +396,7 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
     const int t_in = row / rs.rep;                  // this row's position and head within the tile
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     uint32_t sph = 0, oph = 0, mph = 0;
+    const int score_tiles = (rs.max_len + rs.T + 127) / 128;
     bool merged = false;                            // a join is open: the other warpgroup may still read O
     run.start(tiles_of.items(), tiles_of.mult(), tiles_of, blockIdx.x, gridDim.x);
     while (run.next(tiles_of, seg, w0, w1)) {
@@ -420,6 +429,13 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
           m1 = flash_row_max<false>(rb, key0 + 32, last, 0);
           m2 = flash_row_max<false>(rc, key0 + 64, last, 0);
           m3 = flash_row_max<false>(rd, key0 + 96, last, 0);
+        }
+        if (!TREE && !PAIR && rs.scores && t_in < rs.qpt && t < rs.T) {
+          float* sc = rs.scores + ((size_t)(b * rs.KV + g) * rs.rep * rs.T + row) * ((size_t)score_tiles << 7) + key0;
+          rows_put_scores(ra, sc, rs.scale_log2);
+          rows_put_scores(rb, sc + 32, rs.scale_log2);
+          rows_put_scores(rc, sc + 64, rs.scale_log2);
+          rows_put_scores(rd, sc + 96, rs.scale_log2);
         }
         const float m_tile = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * rs.scale_log2;
         // the slot's previous P.V is complete: its S was issued behind it
@@ -600,23 +616,56 @@ __device__ __forceinline__ void store4(bf16* p, float a, float b, float c, float
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-// Adds the pieces of one row of segment seg to acc (whole warp); how many there were.
+// Joins the pieces of one row of segment seg into acc (whole warp; acc is empty
+// before); how many there were.  A lane per piece gathers the (m, l), so the
+// loads of all pieces are in flight together, and so are those of their O.
 template <int HD, bool TREE>
-__device__ __forceinline__ int join_pieces(const RowsShape& rs, const FlatSeg& seg, long long per, int rrow,
-                                           RowAcc& acc) {
+__device__ __forceinline__ int join_pieces(const RowsShape& rs, const FlatSeg& seg, int per, int rrow, RowAcc& acc) {
   const RowsTiles<TREE> tiles_of{rs};
   const int lane = threadIdx.x & 31, R = rs.slots * rs.tile_rows;
+  const int c0 = seg.s0 / per, c1 = (seg.end() - 1) / per;
   int pieces = 0;
-  for (int c = (int)(seg.s0 / per); c <= (int)((seg.end() - 1) / per); ++c) {
-    int w0, w1;
-    if (!seg.cut(c * per, (c + 1) * per, w0, w1)) continue;
-    if (!TREE && w0 == 0 && w1 == seg.n) return 1;   // whole: written by its CTA, no record
-    const size_t id = tiles_of.record(seg, c, c * per);
-    const float2 ml = *reinterpret_cast<const float2*>(rs.part_ml + (id * R + rrow) * 2);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (lane < HD / 4) o = load4(rs.part_o + ((id * (HD / 4) + lane) * R + rrow) * 4);
-    acc.add(ml.x, ml.y, o);
-    ++pieces;
+  for (int cb = c0; cb <= c1; cb += 32) {
+    const int c = cb + lane;
+    int w0 = 0, w1 = 0;
+    const bool some = c <= c1 && seg.cut(c * per, (c + 1) * per, w0, w1);
+    // a whole segment was written by its CTA and has no record
+    if (!TREE && __any_sync(0xffffffffu, some && w0 == 0 && w1 == seg.n)) return 1;
+    const int id = some ? tiles_of.record(seg, c, c * per) : 0;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (some) ml = *reinterpret_cast<const float2*>(rs.part_ml + ((size_t)id * R + rrow) * 2);
+    pieces += __popc(__ballot_sync(0xffffffffu, some));
+    // pieces in which the row saw no key have nothing in their O
+    uint32_t todo = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
+    const float mn = fmaxf(acc.m, warp_max(ml.x));
+    if (mn == -INFINITY) continue;
+    const float f = acc.m == -INFINITY ? 0.f : exp2f(acc.m - mn);
+    const float fp = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
+    acc.l = acc.l * f + warp_sum(ml.y * fp);
+    acc.m = mn;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc.a[k] *= f;
+    while (todo) {
+      float4 o[4];
+      float w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int l = todo ? __ffs(todo) - 1 : 0;
+        w[u] = __shfl_sync(0xffffffffu, fp, l);
+        const int from = __shfl_sync(0xffffffffu, id, l);
+        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!todo) w[u] = 0.f;
+        if (todo && lane < HD / 4) o[u] = load4(rs.part_o + (((size_t)from * (HD / 4) + lane) * R + rrow) * 4);
+        todo &= todo - 1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        acc.a[0] = fmaf(o[u].x, w[u], acc.a[0]);
+        acc.a[1] = fmaf(o[u].y, w[u], acc.a[1]);
+        acc.a[2] = fmaf(o[u].z, w[u], acc.a[2]);
+        acc.a[3] = fmaf(o[u].w, w[u], acc.a[3]);
+      }
+    }
   }
   return pieces;
 }
@@ -672,14 +721,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   seg.n = rs.G > 0 ? tiles_of(b) : 0;
   if (seg.n > 0) {
     const int mult = tiles_of.mult();
-    const long long per = (flat_total(rs.B, mult, tiles_of) + rs.G - 1) / rs.G;
-    long long before = 0;
+    const int per = (flat_total(rs.B, mult, tiles_of) + rs.G - 1) / rs.G;
+    int before = 0;
     for (int i = lane; i < b; i += 32) before += flat_cost(tiles_of(i));
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) before += __shfl_xor_sync(0xffffffffu, before, s);
+    before = __reduce_add_sync(0xffffffffu, before);
     const int rt = t / rs.qpt, grp = rt / rs.slots;
     seg.sub = grp * rs.KV + g;
-    seg.s0 = before * mult + (long long)seg.sub * flat_cost(seg.n);
+    seg.s0 = before * mult + seg.sub * flat_cost(seg.n);
     join_pieces<HD, true>(rs, seg, per, (rt - grp * rs.slots) * rs.tile_rows + r - rt * rs.qpt * rs.rep, acc);
   }
   float4 qv = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -719,8 +767,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) causal_join_kernel(const __gr
   griddep_wait_and_release();
   const RowsTiles<false> tiles_of{rs};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long total = flat_total(tiles_of.items(), tiles_of.mult(), tiles_of);
-  const long long per = (total + rs.G - 1) / rs.G, pos = (blockIdx.x + 1) * per;
+  const int total = flat_total(tiles_of.items(), tiles_of.mult(), tiles_of);
+  const int per = (total + rs.G - 1) / rs.G, pos = (blockIdx.x + 1) * per;
   if (pos >= total) return;
   const FlatSeg seg = flat_seek(tiles_of.items(), tiles_of.mult(), tiles_of, pos);
   if (seg.s0 == pos || seg.s0 < pos - per) return;

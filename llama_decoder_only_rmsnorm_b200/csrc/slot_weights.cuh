@@ -6,25 +6,33 @@
 // S^T = K Q^T with the 128 keys of a tile on the accumulator's lanes and 128
 // packed rows (position x head, as in rows_attention.cuh) on its columns.  A
 // thread owns one slot and adds up its columns in registers: no shuffle, no
-// atomic, one order for every run.  K stays in shared memory for the whole
-// segment while the query tiles stream past, four accumulators deep; two
-// warpgroups take alternate tiles.  The bound is the exponential unit: 16 per
-// cycle and SM against 128 x 128 per tile, so part of the exponentials goes to
-// the FMA pipe (the fine polynomial: the sums are fp32 results).
+// atomic, one order for every run.  A segment is two key tiles, one per
+// warpgroup; they stay in shared memory while the query tiles stream past, each
+// read once for both (a single key tile per query tile would ask the L2 for 64
+// bytes per cycle and SM: 421 us against @PAIR@ us on the 8B prompt of 8192).
+// The bound is the exponential unit: 16 per cycle and SM, so a quarter of the
+// exponentials goes to the FMA pipe (the fine polynomial: the sums are fp32
+// results).
+//
+// A few rows over a long cache (a decode step) leave their scores in the
+// workspace instead, and scored_weights_kernel below adds them up: K is then
+// not read a second time.
 #pragma once
 #include "rows_attention.cuh"
 
 namespace l3 {
 
 struct WeightShape {
-  int B, S, KV, rep, qpt, tiles, tile_rows, key_tiles, key_shift, G, max_len, cap;
+  int B, S, KV, rep, qpt, tiles, tile_rows;
+  int key_tiles, key_shift;   // segments per (sequence, KV head), log2 of their slots (8 or 6)
+  int G, max_len, cap;
   float scale_log2;
   const int32_t *kv_lens, *seq_lens, *positions;
-  const float* nlse;
+  const float *nlse, *scores;
   const float* win;
   float* wout;
   int32_t* slot_pos;
-  float* part;          // [2 G][key tile]: sums of cut segments
+  float* part;          // [2 G][slots of a segment]: sums of cut segments
 };
 
 // Query tiles that see key tile i % key_tiles of sequence i / key_tiles.
@@ -41,7 +49,7 @@ struct WeightTiles {
     return (live + ws.qpt - 1) / ws.qpt - max(0, key0 - len) / ws.qpt;
   }
   __device__ __forceinline__ int items() const { return ws.B * ws.key_tiles; }
-  __device__ __forceinline__ int record(const FlatSeg& s, int c, long long a) const {
+  __device__ __forceinline__ int record(const FlatSeg& s, int c, int a) const {
     return 2 * c + (s.s0 < a ? 0 : 1);
   }
 };
@@ -59,14 +67,14 @@ struct WeightCfg {
   static constexpr int CHUNKS = (HD + 63) / 64;
   static constexpr int TILE = 128 * 128;
   static constexpr int K_BYTES = CHUNKS * TILE;
+  static constexpr int KRING = 3;                        // a segment's two key tiles and the next one's first
   static constexpr int Q_STAGE = CHUNKS * TILE + 1024;   // 128 rows of q and their 128 log-sum-exps
-  static constexpr int RING0 = (232448 - 1024 - 2048 - 1024 - 2 * K_BYTES) / Q_STAGE;
+  static constexpr int RING0 = (232448 - 1024 - 1024 - KRING * K_BYTES) / Q_STAGE;
   static constexpr int RING = RING0 > 6 ? 6 : RING0;
   static constexpr int OFF_K = 0;
-  static constexpr int OFF_Q = 2 * K_BYTES;
-  static constexpr int OFF_SUM = OFF_Q + RING * Q_STAGE;   // [2][128] floats of the second warpgroup
-  static constexpr int OFF_BAR = OFF_SUM + 1024;
-  static constexpr int N_BARS = 4 + 2 * RING + 8 + 1;
+  static constexpr int OFF_Q = KRING * K_BYTES;
+  static constexpr int OFF_BAR = OFF_Q + RING * Q_STAGE;
+  static constexpr int N_BARS = 2 * KRING + 2 * RING + 8;
   static constexpr int SMEM_BYTES = 1024 + OFF_BAR + N_BARS * 8 + 16;
   static_assert(SMEM_BYTES <= 232448 && RING >= 3, "shared memory");
 };
@@ -110,19 +118,17 @@ __global__ void __launch_bounds__(384, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* k_empty = k_full + 2;
-  uint64_t* q_full = k_empty + 2;
+  uint64_t* k_empty = k_full + C::KRING;
+  uint64_t* q_full = k_empty + C::KRING;
   uint64_t* q_empty = q_full + C::RING;
-  uint64_t* s_full = q_empty + C::RING;
+  uint64_t* s_full = q_empty + C::RING;    // [warpgroup][2]
   uint64_t* s_empty = s_full + 4;
-  uint64_t* swap = s_empty + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(swap + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_empty + 4);
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
-    for (int i = 0; i < C::RING; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1 + 4); }
+    for (int i = 0; i < C::KRING; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
+    for (int i = 0; i < C::RING; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1 + 8); }
     for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 4); }
-    mbar_init(swap, 256);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) { prefetch_tensormap(&mapQ); prefetch_tensormap(&mapK); }
@@ -145,15 +151,18 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true;
       const uint32_t bytes = (uint32_t)(ws.rep * ws.qpt * 128 * C::CHUNKS + 512);
       while (ok && run.next(tiles_of, seg, w0, w1)) {
-        const int b = seg.item / ws.key_tiles, key0 = (seg.item % ws.key_tiles) * 128, g = seg.sub;
+        const int b = seg.item / ws.key_tiles, key0 = (seg.item % ws.key_tiles) * 256, g = seg.sub;
         const int rt0 = tiles_of.first(seg.item);
-        if (!mbar_wait(&k_empty[ks], kph ^ 1u, wait_ns)) break;
-        mbar_arrive_expect_tx(&k_full[ks], C::K_BYTES);
-        for (int c = 0; c < C::CHUNKS; ++c)
-          tma_load_4d(smem + C::OFF_K + ks * C::K_BYTES + c * C::TILE, &mapK, &k_full[ks], c * 64, g, key0, b);
-        kiss |= 1u << ks; kpar = (kpar & ~(1u << ks)) | (kph << ks);
-        if (++ks == 2) { ks = 0; kph ^= 1u; }
-        for (int w = w0; w < w1; ++w) {
+        for (int h = 0; h < 2 && ok; ++h) {
+          if (!mbar_wait(&k_empty[ks], kph ^ 1u, wait_ns)) { ok = false; break; }
+          mbar_arrive_expect_tx(&k_full[ks], C::K_BYTES);
+          for (int c = 0; c < C::CHUNKS; ++c)
+            tma_load_4d(smem + C::OFF_K + ks * C::K_BYTES + c * C::TILE, &mapK, &k_full[ks], c * 64, g,
+                        key0 + h * 128, b);
+          kiss |= 1u << ks; kpar = (kpar & ~(1u << ks)) | (kph << ks);
+          if (++ks == C::KRING) { ks = 0; kph ^= 1u; }
+        }
+        for (int w = w0; w < w1 && ok; ++w) {
           if (!mbar_wait(&q_empty[st], ph ^ 1u, wait_ns)) { ok = false; break; }
           uint8_t* q = smem + C::OFF_Q + st * C::Q_STAGE;
           mbar_arrive_expect_tx(&q_full[st], bytes);
@@ -165,7 +174,7 @@ __global__ void __launch_bounds__(384, 1)
           if (++st == C::RING) { st = 0; ph ^= 1u; }
         }
       }
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < C::KRING; ++s)
         if (kiss & (1u << s)) mbar_wait(&k_full[s], (kpar >> s) & 1u, wait_ns);
       for (int s = 0; s < C::RING; ++s)
         if (iss & (1u << s)) mbar_wait(&q_full[s], (par >> s) & 1u, wait_ns);
@@ -176,54 +185,62 @@ __global__ void __launch_bounds__(384, 1)
     run.start(tiles_of.items(), ws.KV, tiles_of, blockIdx.x, gridDim.x);
     const bool leader = elect_one_sync();
     int st = 0, ks = 0;
-    uint32_t ph = 0, kph = 0, i = 0;   // i: query tiles so far; buffer i & 3
+    uint32_t ph = 0, kph = 0, i = 0;   // i: query tiles so far; buffer i & 1 of each warpgroup
     bool ok = true;
     while (ok && run.next(tiles_of, seg, w0, w1)) {
-      if (!mbar_wait_warp(&k_full[ks], kph, wait_ns)) break;
-      const uint32_t ka = smem_u32(smem + C::OFF_K + ks * C::K_BYTES);
-      for (int w = w0; w < w1; ++w, ++i) {
-        if (!mbar_wait_warp(&q_full[st], ph, wait_ns) || !mbar_wait_warp(&s_empty[i & 3], ((i >> 2) & 1u) ^ 1u, wait_ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+      int kst[2];
+      for (int h = 0; h < 2; ++h) {
+        if (!mbar_wait_warp(&k_full[ks], kph, wait_ns)) ok = false;
+        kst[h] = ks;
+        if (++ks == C::KRING) { ks = 0; kph ^= 1u; }
+      }
+      for (int w = w0; w < w1 && ok; ++w, ++i) {
+        if (!mbar_wait_warp(&q_full[st], ph, wait_ns)) { ok = false; break; }
         const uint32_t qa = smem_u32(smem + C::OFF_Q + st * C::Q_STAGE);
-        if (leader) {
+        for (int h = 0; h < 2; ++h) {
+          const int buf = h * 2 + (i & 1);
+          if (!mbar_wait_warp(&s_empty[buf], ((i >> 1) & 1u) ^ 1u, wait_ns)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t ka = smem_u32(smem + C::OFF_K + kst[h] * C::K_BYTES);
+          if (leader) {
 #pragma unroll
-          for (int k = 0; k < HD / 16; ++k) {
-            const uint32_t off = (k >> 2) * C::TILE + (k & 3) * 32;
-            tc_mma_f16_ss(tmem_base + (i & 3) * 128, sw128_desc(ka + off, 1024, 16), sw128_desc(qa + off, 1024, 16),
-                          IDESC, k > 0);
+            for (int k = 0; k < HD / 16; ++k) {
+              const uint32_t off = (k >> 2) * C::TILE + (k & 3) * 32;
+              tc_mma_f16_ss(tmem_base + buf * 128, sw128_desc(ka + off, 1024, 16), sw128_desc(qa + off, 1024, 16),
+                            IDESC, k > 0);
+            }
+            tc_commit(&s_full[buf]);
           }
-          tc_commit(&s_full[i & 3]);
-          tc_commit(&q_empty[st]);
+          __syncwarp();
         }
+        if (!ok) break;
+        if (leader) tc_commit(&q_empty[st]);
         __syncwarp();
         if (++st == C::RING) { st = 0; ph ^= 1u; }
       }
       if (!ok) break;
-      if (leader) tc_commit(&k_empty[ks]);
+      if (leader) {
+        tc_commit(&k_empty[kst[0]]);
+        tc_commit(&k_empty[kst[1]]);
+      }
       __syncwarp();
-      if (++ks == 2) { ks = 0; kph ^= 1u; }
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- sums (one thread per slot)
     const int wg = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    float* other = reinterpret_cast<float*>(smem + C::OFF_SUM);
+    const uint32_t s_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + wg * 256;
     run.start(tiles_of.items(), ws.KV, tiles_of, blockIdx.x, gridDim.x);
-    uint32_t i = 0, pieces = 0;
+    int st = 0;
+    uint32_t i = 0, ph = 0;
     bool ok = true;
     while (ok && run.next(tiles_of, seg, w0, w1)) {
-      const int b = seg.item / ws.key_tiles, key0 = (seg.item % ws.key_tiles) * 128, g = seg.sub;
+      const int b = seg.item / ws.key_tiles, key0 = (seg.item % ws.key_tiles) * 256 + wg * 128, g = seg.sub;
       const int key = key0 + row, rt0 = tiles_of.first(seg.item);
       const int len = cached_len(ws.kv_lens, b, ws.max_len), live = cached_len(ws.seq_lens, b, ws.S);
       float sum = 0.f;
       for (int w = w0; w < w1; ++w, ++i) {
-        if ((int)(i & 1u) != wg) continue;
-        const int st = i % C::RING;
-        if (!mbar_wait_warp(&s_full[i & 3], (i >> 2) & 1u, wait_ns) ||
-            !mbar_wait_warp(&q_full[st], (i / C::RING) & 1u, wait_ns)) {
+        const int buf = wg * 2 + (i & 1);
+        if (!mbar_wait_warp(&q_full[st], ph, wait_ns) || !mbar_wait_warp(&s_full[buf], (i >> 1) & 1u, wait_ns)) {
           ok = false;
           break;
         }
@@ -233,42 +250,43 @@ __global__ void __launch_bounds__(384, 1)
         const int lo = max(0, key - len - t0) * ws.rep;
         const bool masked = hi < 128 || key0 + 127 > len + t0;
         const float* nlse = reinterpret_cast<const float*>(smem + C::OFF_Q + st * C::Q_STAGE + C::CHUNKS * C::TILE);
-        const uint32_t s_tmem = tmem_base + lane_off + (i & 3) * 128;
-        uint32_t ra[32], rb[32], rc[32], rd[32];
-        flash_load_row(s_tmem, ra, rb, rc, rd);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[i & 3]);
+        const uint32_t s_tmem = s_base + (i & 1) * 128;
         float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+        // two chunks of 32 columns at a time, the next two on their way meanwhile
+        uint32_t ra[32], rb[32];
+        tmem_ld32(s_tmem, ra);
+        tmem_ld32(s_tmem + 32, rb);
+        tc_wait_ld();
         if (masked) {
           weight_add<true>(ra, nlse, 0, lo, hi, ws.scale_log2, a0, a1);
           weight_add<true>(rb, nlse, 32, lo, hi, ws.scale_log2, a2, a3);
-          weight_add<true>(rc, nlse, 64, lo, hi, ws.scale_log2, a0, a1);
-          weight_add<true>(rd, nlse, 96, lo, hi, ws.scale_log2, a2, a3);
         } else {
           weight_add<false>(ra, nlse, 0, lo, hi, ws.scale_log2, a0, a1);
           weight_add<false>(rb, nlse, 32, lo, hi, ws.scale_log2, a2, a3);
-          weight_add<false>(rc, nlse, 64, lo, hi, ws.scale_log2, a0, a1);
-          weight_add<false>(rd, nlse, 96, lo, hi, ws.scale_log2, a2, a3);
+        }
+        tmem_ld32(s_tmem + 64, ra);
+        tmem_ld32(s_tmem + 96, rb);
+        tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[buf]);
+        if (masked) {
+          weight_add<true>(ra, nlse, 64, lo, hi, ws.scale_log2, a0, a1);
+          weight_add<true>(rb, nlse, 96, lo, hi, ws.scale_log2, a2, a3);
+        } else {
+          weight_add<false>(ra, nlse, 64, lo, hi, ws.scale_log2, a0, a1);
+          weight_add<false>(rb, nlse, 96, lo, hi, ws.scale_log2, a2, a3);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_empty[st]);
+        if (++st == C::RING) { st = 0; ph ^= 1u; }
         sum += (a0 + a1) + (a2 + a3);    // tile by tile: two short sums instead of one long one
       }
       if (!ok) break;
-      // the second warpgroup's sums join the first's.  Its buffer is used again two
-      // pieces on, behind a meeting that the first warpgroup comes to after reading it.
-      float* buf = other + (pieces & 1u) * 128;
-      if (wg == 1) buf[row] = sum;
-      mbar_arrive(swap);
-      if (!mbar_wait_warp(swap, pieces & 1u, wait_ns)) break;
-      ++pieces;
-      if (wg == 1) continue;
-      sum += buf[row];
       if (w0 == 0 && w1 == seg.n)
         put_weight(ws, b, g, key, len, live, sum);
       else
-        ws.part[(size_t)tiles_of.record(seg, blockIdx.x, run.a) * 128 + row] = sum;
+        ws.part[(size_t)tiles_of.record(seg, blockIdx.x, run.a) * 256 + wg * 128 + row] = sum;
     }
   }
   tc_fence_before();
@@ -279,10 +297,27 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
+// The weights from scores that the attention kernel left in the workspace (few
+// rows): a thread per slot, over the sequence's rows and the group's heads.
+__global__ void __launch_bounds__(256) scored_weights_kernel(const __grid_constant__ WeightShape ws) {
+  griddep_wait_and_release();
+  const int b = blockIdx.y / ws.KV, g = blockIdx.y % ws.KV, key = blockIdx.x * 256 + threadIdx.x;
+  const int len = cached_len(ws.kv_lens, b, ws.max_len), live = cached_len(ws.seq_lens, b, ws.S);
+  if (key >= len + live) return;
+  const size_t ld = (size_t)((ws.max_len + ws.S + 127) / 128) * 128;
+  const float* sc = ws.scores + (size_t)blockIdx.y * ws.rep * ws.S * ld + key;
+  const float* nlse = ws.nlse + (size_t)blockIdx.y * ws.tile_rows;
+  const int rows = live * ws.rep;       // the packed rows of live positions come first
+  float sum = 0.f;
+#pragma unroll 8
+  for (int r = 0; r < rows; ++r) sum += exp2f(sc[r * ld] + nlse[r]);
+  put_weight(ws, b, g, key, len, live, sum);
+}
+
 // The slots of cut segments: block i < G - 1 takes the segment whose first border
 // is that between CTAs i and i + 1, adding its pieces in order.  Block G - 1 + b
 // carries sequence b's weights over where it has no row in this call.
-__global__ void __launch_bounds__(128) slot_weights_join_kernel(const __grid_constant__ WeightShape ws) {
+__global__ void __launch_bounds__(256) slot_weights_join_kernel(const __grid_constant__ WeightShape ws) {
   griddep_wait_and_release();
   const WeightTiles tiles_of{ws};
   if ((int)blockIdx.x >= ws.G - 1) {
@@ -290,12 +325,12 @@ __global__ void __launch_bounds__(128) slot_weights_join_kernel(const __grid_con
     const int len = cached_len(ws.kv_lens, b, ws.max_len);
     if (cached_len(ws.seq_lens, b, ws.S) > 0) return;
     for (int g = 0; g < ws.KV; ++g)
-      for (int key = threadIdx.x; key < len; key += 128) put_weight(ws, b, g, key, len, 0, 0.f);
+      for (int key = threadIdx.x; key < len; key += 256) put_weight(ws, b, g, key, len, 0, 0.f);
     return;
   }
   const int KT = 1 << ws.key_shift;
-  const long long total = flat_total(tiles_of.items(), ws.KV, tiles_of);
-  const long long per = (total + ws.G - 1) / ws.G, pos = (long long)(blockIdx.x + 1) * per;
+  const int total = flat_total(tiles_of.items(), ws.KV, tiles_of);
+  const int per = (total + ws.G - 1) / ws.G, pos = (int)(blockIdx.x + 1) * per;
   if (pos >= total) return;
   const FlatSeg seg = flat_seek(tiles_of.items(), ws.KV, tiles_of, pos);
   if (seg.s0 == pos || seg.s0 < pos - per) return;
