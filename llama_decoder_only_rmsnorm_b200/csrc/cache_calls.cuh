@@ -218,7 +218,7 @@ int run_observe(const llama3_config* c, RowsPlan& p, const ObserveArgs& a, cudaS
       static bool done[kMaxDevices];
       L3_TRY(opt_in_smem(kern, WeightCfg<HD>::SMEM_BYTES, done));
       L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
-                launch_k(kern, w.G, 384, WeightCfg<HD>::SMEM_BYTES, st, mq, mk, w, wait_ns()));
+                launch_k(kern, w.G, kWeightThreads, WeightCfg<HD>::SMEM_BYTES, st, mq, mk, w, wait_ns()));
       L3_TRY(launch_check());
       launched = true;
     }
@@ -374,10 +374,8 @@ int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src
   L3_TRY(llama3_evict_workspace_size(cfg, n_layers, batch, max_len, budget, &need));
   if (!ws || ws_bytes < need) return LLAMA3_ERR_WORKSPACE;
   if (!aligned16(ws)) return LLAMA3_ERR_ALIGN;
-  // the kernels count rows of one launch, and 16-byte pieces of one row, in 32 bits
-  if ((long long)std::min(n_layers, kEvictLayers) * batch * cfg->n_kv_heads > INT_MAX ||
-      (long long)std::min(max_len, budget) * 32 > INT_MAX / 2)
-    return LLAMA3_ERR_ARG;
+  // the kernels count the rows of one launch in 32 bits
+  if ((long long)std::min(n_layers, kEvictLayers) * batch * cfg->n_kv_heads > INT_MAX) return LLAMA3_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const long long words = evict_row_words(max_len, budget);
   EvictParams p;
@@ -410,10 +408,10 @@ int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src
     L3_LAUNCH(LLAMA3_KERNEL_EVICT, st,
               launch_k(stored ? evict_select_kernel<true> : evict_select_kernel<false>, rows, threads, smem, st, p));
     L3_TRY(launch_check());
-    // parts of a row: enough blocks to fill the GPU, of at least four pieces per thread
-    const long long pieces = (long long)p.from_words * p.row16;
-    const int parts = (int)std::max(1LL, std::min((pieces + 1023) / 1024, 64LL));
-    L3_LAUNCH(LLAMA3_KERNEL_EVICT, st, launch_k(evict_move_kernel, dim3(rows, parts), 256, 0, st, p));
+    // at least four pieces per thread
+    const long long pieces = (long long)(dst ? p.from_words : p.move_words) * p.row16 * p.KV;
+    const int parts = (int)std::max(1LL, std::min((pieces + 1023) / 1024, 1024LL));
+    L3_LAUNCH(LLAMA3_KERNEL_EVICT, st, launch_k(evict_move_kernel, dim3(nl * batch, parts), 256, 0, st, p));
     L3_TRY(launch_check());
   }
   return LLAMA3_OK;

@@ -112,7 +112,26 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant
     for (int i = threadIdx.x; i < left; i += NT) from[i] = i;
     return;
   }
-  if (STORED) {
+  // Counting needs no order: up to 16 keys per thread stay in registers for it.
+  uint32_t own[16];
+  const bool in_regs = STORED && n <= 16 * NT;
+  if (in_regs) {
+    float wv[16];
+    int32_t pv[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      const int j = threadIdx.x + u * NT;
+      wv[u] = j < n ? w[j] : 0.f;
+      pv[u] = j < n ? pos[j] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      const int j = threadIdx.x + u * NT;
+      own[u] = j < n ? evict_key(wv[u], pv[u], floor_pos) : 0u;   // 0 is below every threshold
+      if (j < n) evict_keys[j] = own[u];
+    }
+    __syncthreads();
+  } else if (STORED) {
     for (int j = threadIdx.x; j < n; j += NT) evict_keys[j] = evict_key(w[j], pos[j], floor_pos);
     __syncthreads();
   }
@@ -124,11 +143,20 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant
   for (int shift = 30, look = 0; shift >= 0; shift -= 2, look ^= 1) {
     const uint32_t t1 = cut | (1u << shift), t2 = cut | (2u << shift), t3 = cut | (3u << shift);
     int c1 = 0, c2 = 0, c3 = 0;
-    for (int j = j0; j < j1; ++j) {
-      const uint32_t k = key_at(j);
-      c1 += k >= t1;
-      c2 += k >= t2;
-      c3 += k >= t3;
+    if (in_regs) {
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        c1 += own[u] >= t1;
+        c2 += own[u] >= t2;
+        c3 += own[u] >= t3;
+      }
+    } else {
+      for (int j = j0; j < j1; ++j) {
+        const uint32_t k = key_at(j);
+        c1 += k >= t1;
+        c2 += k >= t2;
+        c3 += k >= t3;
+      }
     }
     c1 = __reduce_add_sync(0xffffffffu, c1);
     c2 = __reduce_add_sync(0xffffffffu, c2);
@@ -182,52 +210,56 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant
   if (threadIdx.x == 0) ws[0] = all_holes;
 }
 
-// Copies the kept slots: blockIdx.x = row, blockIdx.y = part of the row's slots.
-// Four 16-byte pieces of K and of V in flight per thread.  The last launch of a
-// call also writes the lengths: kv_lens_out may be kv_lens, whose shortened
+// Copies the kept slots: blockIdx.x = (layer, sequence), blockIdx.y = part of its
+// slots.  The KV heads' pieces of one slot lie side by side, so a block takes all
+// heads of its slots and the stores are contiguous although every head keeps other
+// slots.  Four 16-byte pieces of K and of V in flight per thread.  The last launch
+// of a call also writes the lengths: kv_lens_out may be kv_lens, whose shortened
 // values give every block here the same `left`.
 __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictParams p) {
   griddep_wait_and_release();
-  const int row = blockIdx.x, g = row % p.KV, b = (row / p.KV) % p.B, layer = row / (p.KV * p.B);
+  const int b = blockIdx.x % p.B, layer = blockIdx.x / p.B;
   const EvictLayer& L = p.layer[layer];
-  const int left = min(cached_len(p.kv_lens, b, p.max_len), p.budget);
-  if (p.lens_out && row == b * p.KV && blockIdx.y == 0 && threadIdx.x == 0) p.lens_out[b] = left;
-  const int32_t* ws = p.ws + (size_t)row * p.ws_row;
-  const int32_t* from = ws + 4;
-  const int32_t* holes = ws + 4 + p.from_words;
-  const int moves = p.in_place ? ws[0] : left;
-  const size_t sbase = ((size_t)b * p.KV + g) * p.cap, dbase = ((size_t)b * p.KV + g) * p.dst_cap;
-  const int total = moves * p.row16, step = 256 * gridDim.y;
-  for (int i0 = blockIdx.y * 256 + threadIdx.x; i0 < total; i0 += 4 * step) {
+  const int len = cached_len(p.kv_lens, b, p.max_len), left = min(len, p.budget);
+  if (p.lens_out && layer == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.lens_out[b] = left;
+  const int32_t* ws0 = p.ws + (size_t)blockIdx.x * p.KV * p.ws_row;
+  // in place: at most as many moves as slots leave, and fewer in some heads
+  const int most = p.in_place ? min(len - left, left) : left;
+  const int slot16 = p.row16 * p.KV;
+  const long long total = (long long)most * slot16;
+  const int step = 256 * gridDim.y;
+  for (long long i0 = blockIdx.y * 256 + threadIdx.x; i0 < total; i0 += 4 * step) {
     uint4 k[4], v[4];
     int to[4], fr[4], c[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * step;
+      const long long i = i0 + u * step;
       to[u] = -1;
       if (i < total) {
-        const int m = i / p.row16;
-        c[u] = i - m * p.row16;
-        to[u] = p.in_place ? holes[m] : m;
-        fr[u] = from[to[u]];
+        const int m = (int)(i / slot16);
+        c[u] = (int)(i - (long long)m * slot16);
+        const int32_t* ws = ws0 + (size_t)(c[u] / p.row16) * p.ws_row;
+        to[u] = !p.in_place ? m : m < ws[0] ? ws[4 + p.from_words + m] : -1;
+        if (to[u] >= 0) fr[u] = ws[4 + to[u]];
       }
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (to[u] >= 0) {
-        const size_t at = (((size_t)b * p.cap + fr[u]) * p.KV + g) * p.row16 + c[u];
+        const size_t at = ((size_t)b * p.cap + fr[u]) * slot16 + c[u];
         k[u] = L.k[at];
         v[u] = L.v[at];
       }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (to[u] >= 0) {
-        const size_t at = (((size_t)b * p.dst_cap + to[u]) * p.KV + g) * p.row16 + c[u];
+        const size_t at = ((size_t)b * p.dst_cap + to[u]) * slot16 + c[u];
         L.dk[at] = k[u];
         L.dv[at] = v[u];
-        if (c[u] == 0) {
-          L.dw[dbase + to[u]] = L.w[sbase + fr[u]];
-          L.dpos[dbase + to[u]] = L.pos[sbase + fr[u]];
+        if (c[u] % p.row16 == 0) {
+          const size_t head = (size_t)b * p.KV + c[u] / p.row16;
+          L.dw[head * p.dst_cap + to[u]] = L.w[head * p.cap + fr[u]];
+          L.dpos[head * p.dst_cap + to[u]] = L.pos[head * p.cap + fr[u]];
         }
       }
   }

@@ -19,7 +19,10 @@ namespace l3 {
 
 // A segment's start and end (query load, first loads in flight, the result's
 // store) cost about as much as this many of its tiles.
-constexpr int kFlatLead = 2;
+#ifndef L3_LEAD
+#define L3_LEAD 2
+#endif
+constexpr int kFlatLead = L3_LEAD;
 
 __device__ __forceinline__ int flat_cost(int n) { return n > 0 ? n + kFlatLead : 0; }
 

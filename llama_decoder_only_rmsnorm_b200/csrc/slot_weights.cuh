@@ -6,8 +6,8 @@
 // S^T = K Q^T with the 128 keys of a tile on the accumulator's lanes and 128
 // packed rows (position x head, as in rows_attention.cuh) on its columns.  A
 // thread owns one slot and adds up its columns in registers: no shuffle, no
-// atomic, one order for every run.  A segment is two key tiles, one per
-// warpgroup; they stay in shared memory while the query tiles stream past, each
+// atomic, one order for every run.  A segment is two key tiles, and two
+// threads per slot share its columns; the keys stay in shared memory while the query tiles stream past, each
 // read once for both (a single key tile per query tile would ask the L2 for 64
 // bytes per cycle and SM: 421 us against @PAIR@ us on the 8B prompt of 8192).
 // The bound is the exponential unit: 16 per cycle and SM, so a quarter of the
@@ -69,12 +69,13 @@ struct WeightCfg {
   static constexpr int K_BYTES = CHUNKS * TILE;
   static constexpr int KRING = 3;                        // a segment's two key tiles and the next one's first
   static constexpr int Q_STAGE = CHUNKS * TILE + 1024;   // 128 rows of q and their 128 log-sum-exps
-  static constexpr int RING0 = (232448 - 1024 - 1024 - KRING * K_BYTES) / Q_STAGE;
+  static constexpr int RING0 = (232448 - 1024 - 2048 - 1024 - KRING * K_BYTES) / Q_STAGE;
   static constexpr int RING = RING0 > 6 ? 6 : RING0;
   static constexpr int OFF_K = 0;
   static constexpr int OFF_Q = KRING * K_BYTES;
-  static constexpr int OFF_BAR = OFF_Q + RING * Q_STAGE;
-  static constexpr int N_BARS = 2 * KRING + 2 * RING + 8;
+  static constexpr int OFF_SUM = OFF_Q + RING * Q_STAGE;   // [2][key tile][128] sums of the right columns
+  static constexpr int OFF_BAR = OFF_SUM + 2048;
+  static constexpr int N_BARS = 2 * KRING + 2 * RING + 8 + 2;
   static constexpr int SMEM_BYTES = 1024 + OFF_BAR + N_BARS * 8 + 16;
   static_assert(SMEM_BYTES <= 232448 && RING >= 3, "shared memory");
 };
@@ -110,8 +111,9 @@ __device__ __forceinline__ void weight_add(uint32_t (&r)[32], const float* nlse,
   }
 }
 
+constexpr int kWeightThreads = 128 + 512;
 template <int HD>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(kWeightThreads, 1)
     slot_weights_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                         const __grid_constant__ WeightShape ws, const unsigned long long wait_ns) {
   using C = WeightCfg<HD>;
@@ -121,14 +123,16 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* k_empty = k_full + C::KRING;
   uint64_t* q_full = k_empty + C::KRING;
   uint64_t* q_empty = q_full + C::RING;
-  uint64_t* s_full = q_empty + C::RING;    // [warpgroup][2]
+  uint64_t* s_full = q_empty + C::RING;    // [key tile][2]
   uint64_t* s_empty = s_full + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_empty + 4);
+  uint64_t* meet = s_empty + 4;            // [key tile]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meet + 2);
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::KRING; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
-    for (int i = 0; i < C::RING; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1 + 8); }
-    for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 4); }
+    for (int i = 0; i < C::RING; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1 + 16); }
+    for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 8); }
+    for (int i = 0; i < 2; ++i) mbar_init(&meet[i], 256);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) { prefetch_tensormap(&mapQ); prefetch_tensormap(&mapK); }
@@ -226,56 +230,45 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
     }
   } else if (warp >= 4) {
-    // ---------------------------------------------------------------- sums (one thread per slot)
-    const int wg = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t s_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + wg * 256;
+    // ---------------------------------------------------------------- sums (two threads per slot)
+    const int kt = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;   // key tile, half of the columns
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t s_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + kt * 256 + half * 64;
+    float* right = reinterpret_cast<float*>(smem + C::OFF_SUM) + kt * 128 + row;
     run.start(tiles_of.items(), ws.KV, tiles_of, blockIdx.x, gridDim.x);
     int st = 0;
-    uint32_t i = 0, ph = 0;
+    uint32_t i = 0, ph = 0, pieces = 0;
     bool ok = true;
     while (ok && run.next(tiles_of, seg, w0, w1)) {
-      const int b = seg.item / ws.key_tiles, key0 = (seg.item % ws.key_tiles) * 256 + wg * 128, g = seg.sub;
+      const int b = seg.item / ws.key_tiles, key0 = (seg.item % ws.key_tiles) * 256 + kt * 128, g = seg.sub;
       const int key = key0 + row, rt0 = tiles_of.first(seg.item);
       const int len = cached_len(ws.kv_lens, b, ws.max_len), live = cached_len(ws.seq_lens, b, ws.S);
       float sum = 0.f;
       for (int w = w0; w < w1; ++w, ++i) {
-        const int buf = wg * 2 + (i & 1);
+        const int buf = kt * 2 + (i & 1);
         if (!mbar_wait_warp(&q_full[st], ph, wait_ns) || !mbar_wait_warp(&s_full[buf], (i >> 1) & 1u, wait_ns)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int t0 = (rt0 + w) * ws.qpt;
-        const int hi = min(ws.qpt, live - t0) * ws.rep;
-        const int lo = max(0, key - len - t0) * ws.rep;
-        const bool masked = hi < 128 || key0 + 127 > len + t0;
-        const float* nlse = reinterpret_cast<const float*>(smem + C::OFF_Q + st * C::Q_STAGE + C::CHUNKS * C::TILE);
-        const uint32_t s_tmem = s_base + (i & 1) * 128;
-        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-        // two chunks of 32 columns at a time, the next two on their way meanwhile
         uint32_t ra[32], rb[32];
-        tmem_ld32(s_tmem, ra);
-        tmem_ld32(s_tmem + 32, rb);
-        tc_wait_ld();
-        if (masked) {
-          weight_add<true>(ra, nlse, 0, lo, hi, ws.scale_log2, a0, a1);
-          weight_add<true>(rb, nlse, 32, lo, hi, ws.scale_log2, a2, a3);
-        } else {
-          weight_add<false>(ra, nlse, 0, lo, hi, ws.scale_log2, a0, a1);
-          weight_add<false>(rb, nlse, 32, lo, hi, ws.scale_log2, a2, a3);
-        }
-        tmem_ld32(s_tmem + 64, ra);
-        tmem_ld32(s_tmem + 96, rb);
+        tmem_ld32(s_base + (i & 1) * 128, ra);
+        tmem_ld32(s_base + (i & 1) * 128 + 32, rb);
         tc_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[buf]);
-        if (masked) {
-          weight_add<true>(ra, nlse, 64, lo, hi, ws.scale_log2, a0, a1);
-          weight_add<true>(rb, nlse, 96, lo, hi, ws.scale_log2, a2, a3);
+        const int t0 = (rt0 + w) * ws.qpt;
+        const float* nlse = reinterpret_cast<const float*>(smem + C::OFF_Q + st * C::Q_STAGE + C::CHUNKS * C::TILE);
+        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+        const int hi = min(ws.qpt, live - t0) * ws.rep;
+        if (hi < 128 || key0 + 127 > len + t0) {
+          const int lo = max(0, key - len - t0) * ws.rep;
+          weight_add<true>(ra, nlse, half * 64, lo, hi, ws.scale_log2, a0, a1);
+          weight_add<true>(rb, nlse, half * 64 + 32, lo, hi, ws.scale_log2, a2, a3);
         } else {
-          weight_add<false>(ra, nlse, 64, lo, hi, ws.scale_log2, a0, a1);
-          weight_add<false>(rb, nlse, 96, lo, hi, ws.scale_log2, a2, a3);
+          weight_add<false>(ra, nlse, half * 64, 0, 128, ws.scale_log2, a0, a1);
+          weight_add<false>(rb, nlse, half * 64 + 32, 0, 128, ws.scale_log2, a2, a3);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_empty[st]);
@@ -283,10 +276,19 @@ __global__ void __launch_bounds__(384, 1)
         sum += (a0 + a1) + (a2 + a3);    // tile by tile: two short sums instead of one long one
       }
       if (!ok) break;
-      if (w0 == 0 && w1 == seg.n)
-        put_weight(ws, b, g, key, len, live, sum);
-      else
-        ws.part[(size_t)tiles_of.record(seg, blockIdx.x, run.a) * 256 + wg * 128 + row] = sum;
+      // The right columns' sums join the left ones'.  The buffer is used again two
+      // pieces on, behind a meeting that the left threads come to after reading it.
+      if (half) right[(pieces & 1u) * 256] = sum;
+      mbar_arrive(&meet[kt]);
+      if (!mbar_wait_warp(&meet[kt], pieces & 1u, wait_ns)) break;
+      if (!half) {
+        sum += right[(pieces & 1u) * 256];
+        if (w0 == 0 && w1 == seg.n)
+          put_weight(ws, b, g, key, len, live, sum);
+        else
+          ws.part[(size_t)tiles_of.record(seg, blockIdx.x, run.a) * 256 + kt * 128 + row] = sum;
+      }
+      ++pieces;
     }
   }
   tc_fence_before();
