@@ -21,7 +21,7 @@ struct RowsPlan {
   RowsShape rs;
   bool tc, pair;
   bool fits;       // the plans' units stay below 2^30
-  size_t ml, o, nlse, sums, scores, total;
+  size_t cuts, ml, o, nlse, sums, scores, total;
   bool scored;     // observed: the weights come from kept scores
 };
 RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len) {
@@ -49,6 +49,7 @@ RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len)
   const size_t records = tree ? (size_t)B * rs.groups * rs.KV + rs.G : (size_t)2 * rs.G;
   const size_t rows = records * rs.slots * rs.tile_rows;
   size_t off = 0;
+  p.cuts = off; off += up256((size_t)2 * num_sms() * sizeof(FlatCut));
   p.ml = off; off += up256(rows * 2 * 4);
   p.o = off; off += up256(rows * c->head_dim * 4);
   if (!tree) {
@@ -155,6 +156,7 @@ int run_tree(const llama3_config* c, RowsPlan& p, const TreeArgs& a, cudaStream_
   RowsShape& rs = p.rs;
   rs.kv_lens = a.kv_lens;
   rs.out = a.out;
+  rs.cuts = ws_at<FlatCut>(a.ws, p.cuts);
   rs.part_ml = ws_at<float>(a.ws, p.ml);
   rs.part_o = ws_at<float>(a.ws, p.o);
   if (rs.G > 0) L3_TRY((run_rows<T, HD, true>(c, p, a.q, a.kc, a.vc, a.cap, st)));
@@ -179,6 +181,7 @@ int run_observe(const llama3_config* c, RowsPlan& p, const ObserveArgs& a, cudaS
   rs.kv_lens = a.kv_lens;
   rs.seq_lens = a.seq_lens;
   rs.out = a.out;
+  rs.cuts = ws_at<FlatCut>(a.ws, p.cuts);
   rs.part_ml = ws_at<float>(a.ws, p.ml);
   rs.part_o = ws_at<float>(a.ws, p.o);
   rs.nlse = ws_at<float>(a.ws, p.nlse);
@@ -186,7 +189,7 @@ int run_observe(const llama3_config* c, RowsPlan& p, const ObserveArgs& a, cudaS
   L3_TRY((run_rows<T, HD, false>(c, p, a.q, a.kc, a.vc, a.cap, st)));
   if (rs.G > 1) {
     L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
-              launch_k((causal_join_kernel<T, HD>), dim3(rs.G - 1, (rs.slots * rs.tile_rows + 63) / 64),
+              launch_k((causal_join_kernel<T, HD>), dim3(rs.G - 1, (rs.slots * rs.tile_rows + kCausalJoinRows - 1) / kCausalJoinRows),
                        32 * kJoinWarps, 0, st, rs));
     L3_TRY(launch_check());
   }
@@ -200,6 +203,7 @@ int run_observe(const llama3_config* c, RowsPlan& p, const ObserveArgs& a, cudaS
   w.nlse = rs.nlse; w.win = a.win; w.wout = a.wout; w.slot_pos = a.slot_pos;
   w.part = ws_at<float>(a.ws, p.sums);
   w.scores = rs.scores;
+  w.cuts = rs.cuts;   // the attention's cuts have been joined when the weights' are written
   if (p.scored) {
     L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
               launch_k(scored_weights_kernel, dim3((rs.max_len + rs.T + 255) / 256, rs.B * rs.KV), 256, 0, st, w));

@@ -19,10 +19,8 @@ namespace l3 {
 
 // A segment's start and end (query load, first loads in flight, the result's
 // store) cost about as much as this many of its tiles.
-#ifndef L3_LEAD
-#define L3_LEAD 2
-#endif
-constexpr int kFlatLead = L3_LEAD;
+// (2, 3, 4 and 6 measure alike, from 8B decode steps to the 8B prompt.)
+constexpr int kFlatLead = 2;
 
 __device__ __forceinline__ int flat_cost(int n) { return n > 0 ? n + kFlatLead : 0; }
 
@@ -79,11 +77,19 @@ __device__ __forceinline__ FlatSeg flat_seek(int items, int mult, const NOf& n_o
   return s;
 }
 
+// What the kernels that join the pieces of cut segments need of the plan, left by
+// the main kernel: entry c is the segment that the border before CTA c's run
+// cuts, if that is the first border within it (n = 0 otherwise), and the run
+// length `per`.
+struct FlatCut {
+  int item, sub, n, s0, per, pad[3];
+};
+
 // The pieces of one CTA, in order.
 template <class NOf>
 struct FlatRun {
   FlatSeg seg;
-  int a, e;
+  int a, e, per;
   int items, mult;
   bool more;
   // Whole warp.
@@ -91,11 +97,18 @@ struct FlatRun {
     items = items_;
     mult = mult_;
     const int total = flat_total(items, mult, n_of);
-    const int per = (total + G - 1) / G;
+    per = (total + G - 1) / G;
     a = per * c;
     e = min(a + per, total);
     more = a < e;
     if (more) seg = flat_seek(items, mult, n_of, a);
+  }
+  // After start(), by one thread of CTA c.
+  __device__ __forceinline__ void leave(FlatCut* cuts, int c) const {
+    const bool first = more && seg.s0 < a && seg.s0 >= a - per;
+    int4* out = reinterpret_cast<int4*>(cuts + c);
+    out[0] = make_int4(more ? seg.item : 0, more ? seg.sub : 0, first ? seg.n : 0, more ? seg.s0 : 0);
+    out[1] = make_int4(per, 0, 0, 0);
   }
   // The next piece, or false at the end of the run (any lane, no communication).
   __device__ __forceinline__ bool next(const NOf& n_of, FlatSeg& s, int& w0, int& w1) {
@@ -117,5 +130,17 @@ struct FlatRun {
     return false;
   }
 };
+
+__device__ __forceinline__ FlatSeg flat_cut(const FlatCut* cuts, int c, int& per) {
+  const int4* in = reinterpret_cast<const int4*>(cuts + c);
+  const int4 x = in[0];
+  per = in[1].x;
+  FlatSeg s;
+  s.item = x.x;
+  s.sub = x.y;
+  s.n = x.z;
+  s.s0 = x.w;
+  return s;
+}
 
 }  // namespace l3

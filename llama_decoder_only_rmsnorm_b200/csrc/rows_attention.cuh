@@ -40,6 +40,7 @@ struct RowsShape {
   int G, max_len;                    // CTAs of the main kernel
   float scale_log2;                  // log2(e) / sqrt(hd)
   const int32_t *kv_lens, *seq_lens;
+  FlatCut* cuts;                     // [G] the plan, for the kernels that join
   float *part_ml, *part_o;           // records: [id][row][2] and [id][hd/4][row][4], slots * tile_rows rows
   float* scores;                     // observed, few rows: [B][H * T][key tiles * 128] in the log2 domain, or NULL
   float* nlse;                       // observed: minus the rows' log-sum-exp (log2), [B * KV][tiles][tile_rows]
@@ -222,10 +223,12 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
       // -------------------------------------------------------------- producer
       run.start(tiles_of.items(), tiles_of.mult(), tiles_of, blockIdx.x, gridDim.x);
       if (lane == 0) {
+        run.leave(rs.cuts, blockIdx.x);
         int st = 0;
         uint32_t ph = 0, qph = 0, iss = 0, par = 0, qiss = 0, qpar = 0;
         bool ok = true;
         const uint32_t q_bytes = (uint32_t)(rs.rep * rs.qpt * 128 * C::CHUNKS);
+        const uint64_t once = policy_evict_first();
         while (ok && run.next(tiles_of, seg, w0, w1)) {
           tiles_of.where(seg, b, grp, g);
           for (int s = 0; s < C::NQ; ++s) {
@@ -244,8 +247,12 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
             if (!mbar_wait(&bars.empty[st], ph ^ 1u, wait_ns)) return false;
             mbar_arrive_expect_tx(&bars.full[st], C::KV_BYTES);
             for (int c = 0; c < C::CHUNKS; ++c)
-              tma_load_4d(smem + C::OFF_RING + st * C::KV_BYTES + c * C::TILE, is_v ? &mapV : &mapK, &bars.full[st],
-                          c * 64, g, (w0 + j) * 128, b);
+              if (rs.groups == 1)   // no other CTA reads this tile: the L2 is for records and scores
+                tma_load_4d_once(smem + C::OFF_RING + st * C::KV_BYTES + c * C::TILE, is_v ? &mapV : &mapK,
+                                 &bars.full[st], c * 64, g, (w0 + j) * 128, b, once);
+              else
+                tma_load_4d(smem + C::OFF_RING + st * C::KV_BYTES + c * C::TILE, is_v ? &mapV : &mapK, &bars.full[st],
+                            c * 64, g, (w0 + j) * 128, b);
             iss |= 1u << st; par = (par & ~(1u << st)) | (ph << st);
             if (++st == C::RING) { st = 0; ph ^= 1u; }
             return true;
@@ -713,6 +720,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     return;
   }
   __syncwarp();
+  // the first four keys of the chain and q are under way while the pieces are joined
+  float4 qv = make_float4(0.f, 0.f, 0.f, 0.f), k[4], v[4];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      k[u] = v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + u < depth && on) {
+        const size_t at = (((size_t)b * rs.T + chain[i0 + u]) * rs.KV + g) * HD + 4 * lane;
+        k[u] = load4(kn + at);
+        v[u] = load4(vn + at);
+      }
+    }
+  };
+  if (on) qv = load4(q + (((size_t)b * rs.T + t) * rs.H + h) * HD + 4 * lane);
+  fetch(0);
   RowAcc acc;
   acc.clear();
   const RowsTiles<true> tiles_of{rs};
@@ -721,7 +743,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   seg.n = rs.G > 0 ? tiles_of(b) : 0;
   if (seg.n > 0) {
     const int mult = tiles_of.mult();
-    const int per = (flat_total(rs.B, mult, tiles_of) + rs.G - 1) / rs.G;
+    const int per = rs.cuts->per;
     int before = 0;
     for (int i = lane; i < b; i += 32) before += flat_cost(tiles_of(i));
     before = __reduce_add_sync(0xffffffffu, before);
@@ -730,23 +752,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     seg.s0 = before * mult + seg.sub * flat_cost(seg.n);
     join_pieces<HD, true>(rs, seg, per, (rt - grp * rs.slots) * rs.tile_rows + r - rt * rs.qpt * rs.rep, acc);
   }
-  float4 qv = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (on) qv = load4(q + (((size_t)b * rs.T + t) * rs.H + h) * HD + 4 * lane);
   // four keys at a time, so that their loads and sums overlap
   for (int i0 = 0; i0 < depth; i0 += 4) {
     float sc[4];
-    float4 v[4];
+    if (i0) fetch(i0);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      sc[u] = 0.f;
-      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + u < depth && on) {
-        const size_t at = (((size_t)b * rs.T + chain[i0 + u]) * rs.KV + g) * HD + 4 * lane;
-        const float4 k = load4(kn + at);
-        v[u] = load4(vn + at);
-        sc[u] = fmaf(qv.x, k.x, fmaf(qv.y, k.y, fmaf(qv.z, k.z, qv.w * k.w)));
-      }
-    }
+    for (int u = 0; u < 4; ++u)
+      sc[u] = fmaf(qv.x, k[u].x, fmaf(qv.y, k[u].y, fmaf(qv.z, k[u].z, qv.w * k[u].w)));
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1)
 #pragma unroll
@@ -760,22 +772,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 }
 
 // Observed attention: the rows of the segments that were cut.  blockIdx.x + 1 is
-// the border between two CTAs' runs; the first border within a segment takes
-// it.  blockIdx.y = 64 rows.
+// the CTA whose border cuts the segment, blockIdx.y = 16 of its rows.
+constexpr int kCausalJoinRows = 16;
 template <typename T, int HD>
 __global__ void __launch_bounds__(32 * kJoinWarps) causal_join_kernel(const __grid_constant__ RowsShape rs) {
   griddep_wait_and_release();
   const RowsTiles<false> tiles_of{rs};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int total = flat_total(tiles_of.items(), tiles_of.mult(), tiles_of);
-  const int per = (total + rs.G - 1) / rs.G, pos = (blockIdx.x + 1) * per;
-  if (pos >= total) return;
-  const FlatSeg seg = flat_seek(tiles_of.items(), tiles_of.mult(), tiles_of, pos);
-  if (seg.s0 == pos || seg.s0 < pos - per) return;
-  int b, grp, g;
+  int per, b, grp, g;
+  const FlatSeg seg = flat_cut(rs.cuts, blockIdx.x + 1, per);
+  if (seg.n == 0) return;
   tiles_of.where(seg, b, grp, g);
   const int live = cached_len(rs.seq_lens, b, rs.T);
-  const int first = blockIdx.y * 64 + warp, end = min(blockIdx.y * 64 + 64, rs.slots * rs.tile_rows);
+  const int first = blockIdx.y * kCausalJoinRows + warp;
+  const int end = min((int)(blockIdx.y + 1) * kCausalJoinRows, rs.slots * rs.tile_rows);
   for (int r = first; r < end; r += kJoinWarps) {
     const int rt = grp * rs.slots + r / rs.tile_rows, in = r % rs.tile_rows;
     const int t_in = in / rs.rep, t = rt * rs.qpt + t_in, h = g * rs.rep + in - t_in * rs.rep;

@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(256) rows_simt_kernel(const __grid_constant__ 
   FlatSeg seg;
   int w0, w1, b, rt, g;
   run.start(tiles_of.items(), tiles_of.mult(), tiles_of, blockIdx.x, gridDim.x);
+  if (threadIdx.x == 0) run.leave(rs.cuts, blockIdx.x);
   while (run.next(tiles_of, seg, w0, w1)) {
     tiles_of.where(seg, b, rt, g);                  // one row tile per group
     const int len = cached_len(rs.kv_lens, b, rs.max_len);
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(256) slot_weights_simt_kernel(const __grid_con
   FlatSeg seg;
   int w0, w1;
   run.start(tiles_of.items(), ws.KV, tiles_of, blockIdx.x, gridDim.x);
+  if (threadIdx.x == 0) run.leave(ws.cuts, blockIdx.x);
   while (run.next(tiles_of, seg, w0, w1)) {
     const int b = seg.item / ws.key_tiles, key0 = (seg.item % ws.key_tiles) * kSimtTile, g = seg.sub;
     const int rt0 = tiles_of.first(seg.item);

@@ -32,6 +32,7 @@ struct WeightShape {
   const float* win;
   float* wout;
   int32_t* slot_pos;
+  FlatCut* cuts;        // [G]
   float* part;          // [2 G][slots of a segment]: sums of cut segments
 };
 
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     // ---------------------------------------------------------------- producer
     run.start(tiles_of.items(), ws.KV, tiles_of, blockIdx.x, gridDim.x);
     if (lane == 0) {
+      run.leave(ws.cuts, blockIdx.x);
       int st = 0, ks = 0;
       uint32_t ph = 0, kph = 0, iss = 0, par = 0, kiss = 0, kpar = 0;
       bool ok = true;
@@ -316,8 +318,8 @@ __global__ void __launch_bounds__(256) scored_weights_kernel(const __grid_consta
   put_weight(ws, b, g, key, len, live, sum);
 }
 
-// The slots of cut segments: block i < G - 1 takes the segment whose first border
-// is that between CTAs i and i + 1, adding its pieces in order.  Block G - 1 + b
+// The slots of cut segments: block i < G - 1 takes the one that CTA i + 1's border
+// cuts, adding its pieces in order.  Block G - 1 + b
 // carries sequence b's weights over where it has no row in this call.
 __global__ void __launch_bounds__(256) slot_weights_join_kernel(const __grid_constant__ WeightShape ws) {
   griddep_wait_and_release();
@@ -331,11 +333,9 @@ __global__ void __launch_bounds__(256) slot_weights_join_kernel(const __grid_con
     return;
   }
   const int KT = 1 << ws.key_shift;
-  const int total = flat_total(tiles_of.items(), ws.KV, tiles_of);
-  const int per = (total + ws.G - 1) / ws.G, pos = (int)(blockIdx.x + 1) * per;
-  if (pos >= total) return;
-  const FlatSeg seg = flat_seek(tiles_of.items(), ws.KV, tiles_of, pos);
-  if (seg.s0 == pos || seg.s0 < pos - per) return;
+  int per;
+  const FlatSeg seg = flat_cut(ws.cuts, blockIdx.x + 1, per);
+  if (seg.n == 0) return;
   const int b = seg.item / ws.key_tiles, key0 = (seg.item % ws.key_tiles) << ws.key_shift;
   const int len = cached_len(ws.kv_lens, b, ws.max_len), live = cached_len(ws.seq_lens, b, ws.S);
   if ((int)threadIdx.x >= KT) return;
