@@ -18,9 +18,9 @@
 namespace l3 {
 
 // A segment's start and end (query load, first loads in flight, the result's
-// store) cost about as much as this many of its tiles.
-// (2, 3, 4 and 6 measure alike, from 8B decode steps to the 8B prompt.)
-constexpr int kFlatLead = 2;
+// store) in tiles: on the 8B prompt a segment costs 9200 cycles beside its tiles
+// of 3350 each.
+constexpr int kFlatLead = 3;
 
 __device__ __forceinline__ int flat_cost(int n) { return n > 0 ? n + kFlatLead : 0; }
 
@@ -85,6 +85,12 @@ struct FlatCut {
   int item, sub, n, s0, per, pad[3];
 };
 
+// A value that all lanes hold, as one that the compiler knows to be the same for
+// the whole warp: loop bounds of the plan come from shuffles, and without this a
+// loop over them counts as divergent, which keeps the tcgen05 issuers' addresses
+// out of the uniform registers.
+__device__ __forceinline__ int warp_uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 // The pieces of one CTA, in order.
 template <class NOf>
 struct FlatRun {
@@ -110,6 +116,17 @@ struct FlatRun {
     out[0] = make_int4(more ? seg.item : 0, more ? seg.sub : 0, first ? seg.n : 0, more ? seg.s0 : 0);
     out[1] = make_int4(per, 0, 0, 0);
   }
+  // next() for a whole warp, with everything uniform.
+  __device__ __forceinline__ bool next_uniform(const NOf& n_of, FlatSeg& s, int& w0, int& w1) {
+    if (!__all_sync(0xffffffffu, next(n_of, s, w0, w1))) return false;
+    s.item = warp_uniform(s.item);
+    s.sub = warp_uniform(s.sub);
+    s.n = warp_uniform(s.n);
+    s.s0 = warp_uniform(s.s0);
+    w0 = warp_uniform(w0);
+    w1 = warp_uniform(w1);
+    return true;
+  }
   // The next piece, or false at the end of the run (any lane, no communication).
   __device__ __forceinline__ bool next(const NOf& n_of, FlatSeg& s, int& w0, int& w1) {
     while (more) {
@@ -128,6 +145,37 @@ struct FlatRun {
       if (some) return true;
     }
     return false;
+  }
+};
+
+// A warp's run in shared memory: lane 0 steps it, all lanes read the piece, so
+// that the plan takes no registers while a warp works on a piece.
+template <class NOf>
+struct FlatBox {
+  FlatRun<NOf> run;
+  FlatSeg seg;
+  int w0, w1;
+  int more;
+  __device__ __forceinline__ void start(int items, int mult, const NOf& n_of, int c, int G) {
+    FlatRun<NOf> r;
+    r.start(items, mult, n_of, c, G);
+    if ((threadIdx.x & 31) == 0) run = r;
+    __syncwarp();
+  }
+  __device__ __forceinline__ bool next(const NOf& n_of) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      FlatRun<NOf> r = run;
+      FlatSeg s = r.seg;
+      int a = 0, b = 0;
+      more = r.next(n_of, s, a, b) ? 1 : 0;
+      run = r;
+      seg = s;
+      w0 = a;
+      w1 = b;
+    }
+    __syncwarp();
+    return more != 0;
   }
 };
 

@@ -116,14 +116,15 @@ __device__ __forceinline__ void exp2_poly2_fine(float x0, float x1, float& y0, f
 }
 
 // p = 2^(s * scl - m) for 32 scores in place and their sum; the FMA pipe takes
-// 4 of 16 pairs of an unmasked row (FINE: with the fine polynomial).
+// 4 of 16 pairs of an unmasked row, or, FINE, 2 with the fine polynomial (8B
+// prompt: 832 k cycles against 872 k with 4 and 839 k with none).
 template <bool MASKED, bool FINE>
 __device__ __forceinline__ void rows_exp(uint32_t (&r)[32], float scl, float neg_m, float& sa, float& sb) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float x0, x1, p0, p1;
     fma2(x0, x1, __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), scl, scl, neg_m, neg_m);
-    if (!MASKED && (i & 7) < 2) {
+    if (!MASKED && (i & 7) < (FINE ? 1 : 2)) {
       if (FINE) exp2_poly2_fine(x0, x1, p0, p1); else exp2_poly2(x0, x1, p0, p1);
     } else {
       p0 = ex2_approx(x0);
@@ -273,6 +274,9 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
       int st = 0;
       uint32_t ph = 0, qph = 0, pph = 0;
       bool ok = true;
+      // PAIR calls name their slot by a literal: addresses and descriptors of the
+      // two slots are then constants of the code, and the next S is ready 1100
+      // cycles after a row's last P instead of 1390 (8B prompt of 8192).
       // the next tile of the ring, once it has landed; -1 if the wait gave up
       auto take = [&]() -> int {
         if (!mbar_wait_warp(&bars.full[st], ph, wait_ns)) return -1;
@@ -297,6 +301,7 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
       // waits for the halves of slot s's P and adds P V; false if a wait gave up
       auto issue_pv = [&](int s, int vst, bool accumulate) -> bool {
         const uint32_t va = ring_addr + vst * C::KV_BYTES;
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!mbar_wait_warp(half ? &bars.p_full[s] : &bars.p_half[s], (pph >> s) & 1u, wait_ns)) return false;
           tc_fence_after();
@@ -323,10 +328,11 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       };
-      while (ok && run.next(tiles_of, seg, w0, w1)) {
+      while (ok && run.next_uniform(tiles_of, seg, w0, w1)) {
         tiles_of.where(seg, b, grp, g);
         const int n = w1 - w0;
-        const int held = cached_len(rs.kv_lens, b, rs.max_len) + (TREE ? 0 : cached_len(rs.seq_lens, b, rs.T));
+        const int held = warp_uniform(cached_len(rs.kv_lens, b, rs.max_len) +
+                                      (TREE ? 0 : cached_len(rs.seq_lens, b, rs.T)));
         const int nslots = PAIR ? (grp * 2 + 1 < rs.tiles ? 2 : 1) : 1;
         for (int s = 0; s < nslots; ++s) {
           if (!mbar_wait_warp(&bars.q_full[s], (qph >> s) & 1u, wait_ns)) ok = false;
@@ -339,7 +345,8 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
           const int kst = take();
           if (kst < 0) return false;
           if (PAIR) {
-            for (int s = 0; s < nslots; ++s) issue_s(s, kst);
+            issue_s(0, kst);
+            if (nslots == 2) issue_s(1, kst);
           } else {
             issue_s(i & 1, kst);
           }
@@ -354,15 +361,16 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
           if ((w0 + j) * 128 + 128 > held) clear_tail(vst, held - (w0 + j) * 128);
           if (PAIR) {
             int kst = -1;
-            for (int s = 0; s < nslots && ok; ++s) {
-              ok = issue_pv(s, vst, j > 0);
-              if (ok && j + 1 < n) {
-                if (s == 0) kst = take();
-                ok = kst >= 0;
-                if (ok) issue_s(s, kst);
-              }
+            if (!issue_pv(0, vst, j > 0)) { ok = false; break; }
+            if (j + 1 < n) {
+              kst = take();
+              if (kst < 0) { ok = false; break; }
+              issue_s(0, kst);
             }
-            if (!ok) break;
+            if (nslots == 2) {
+              if (!issue_pv(1, vst, j > 0)) { ok = false; break; }
+              if (j + 1 < n) issue_s(1, kst);
+            }
             if (leader) {
               tc_commit(&bars.empty[vst]);
               if (kst >= 0) tc_commit(&bars.empty[kst]);
@@ -406,11 +414,11 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
     const int score_tiles = (rs.max_len + rs.T + 127) / 128;
     bool merged = false;                            // a join is open: the other warpgroup may still read O
     run.start(tiles_of.items(), tiles_of.mult(), tiles_of, blockIdx.x, gridDim.x);
-    while (run.next(tiles_of, seg, w0, w1)) {
+    while (run.next_uniform(tiles_of, seg, w0, w1)) {
       tiles_of.where(seg, b, grp, g);
       const int rt = PAIR ? grp * 2 + slot : grp;
       if (PAIR && rt >= rs.tiles) continue;
-      const int len = cached_len(rs.kv_lens, b, rs.max_len);
+      const int len = warp_uniform(cached_len(rs.kv_lens, b, rs.max_len));
       const int t = rt * rs.qpt + t_in;
       const int last = TREE ? len - 1 : len + t;                     // last key this row sees
       const int last_min = TREE ? len - 1 : len + rt * rs.qpt;       // and the tile's first row
@@ -623,68 +631,83 @@ __device__ __forceinline__ void store4(bf16* p, float a, float b, float c, float
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-// Joins the pieces of one row of segment seg into acc (whole warp; acc is empty
-// before); how many there were.  A lane per piece gathers the (m, l), so the
-// loads of all pieces are in flight together, and so are those of their O.
-template <int HD, bool TREE>
-__device__ __forceinline__ int join_pieces(const RowsShape& rs, const FlatSeg& seg, int per, int rrow, RowAcc& acc) {
-  const RowsTiles<TREE> tiles_of{rs};
+// Joins the pieces of NR neighbouring rows of segment seg, from record row rrow on,
+// into acc (whole warp; acc is empty before).  A lane per piece gathers the (m,
+// l), and the first U pieces' O are asked for before those are needed.
+template <int HD, int NR>
+__device__ __forceinline__ void join_pieces(const RowsShape& rs, const FlatSeg& seg, int per, int rrow,
+                                            RowAcc (&acc)[NR]) {
+  constexpr int U = 8 / NR;
+  const RowsTiles<true> tiles_of{rs};
   const int lane = threadIdx.x & 31, R = rs.slots * rs.tile_rows;
   const int c0 = seg.s0 / per, c1 = (seg.end() - 1) / per;
-  int pieces = 0;
   for (int cb = c0; cb <= c1; cb += 32) {
     const int c = cb + lane;
     int w0 = 0, w1 = 0;
     const bool some = c <= c1 && seg.cut(c * per, (c + 1) * per, w0, w1);
-    // a whole segment was written by its CTA and has no record
-    if (!TREE && __any_sync(0xffffffffu, some && w0 == 0 && w1 == seg.n)) return 1;
     const int id = some ? tiles_of.record(seg, c, c * per) : 0;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (some) ml = *reinterpret_cast<const float2*>(rs.part_ml + ((size_t)id * R + rrow) * 2);
-    pieces += __popc(__ballot_sync(0xffffffffu, some));
-    // pieces in which the row saw no key have nothing in their O
-    uint32_t todo = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
-    const float mn = fmaxf(acc.m, warp_max(ml.x));
-    if (mn == -INFINITY) continue;
-    const float f = acc.m == -INFINITY ? 0.f : exp2f(acc.m - mn);
-    const float fp = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
-    acc.l = acc.l * f + warp_sum(ml.y * fp);
-    acc.m = mn;
+    uint32_t todo = __ballot_sync(0xffffffffu, some);
+    float2 ml[NR];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc.a[k] *= f;
-    while (todo) {
-      float4 o[4];
-      float w[4];
+    for (int i = 0; i < NR; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (some) ml[i] = *reinterpret_cast<const float2*>(rs.part_ml + ((size_t)id * R + rrow + i) * 2);
+    }
+    float4 o[U][NR];
+    int src[U];
+    auto fetch = [&]() {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int l = todo ? __ffs(todo) - 1 : 0;
-        w[u] = __shfl_sync(0xffffffffu, fp, l);
-        const int from = __shfl_sync(0xffffffffu, id, l);
-        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!todo) w[u] = 0.f;
-        if (todo && lane < HD / 4) o[u] = load4(rs.part_o + (((size_t)from * (HD / 4) + lane) * R + rrow) * 4);
+      for (int u = 0; u < U; ++u) {
+        src[u] = todo ? __ffs(todo) - 1 : -1;
+        const int from = __shfl_sync(0xffffffffu, id, max(src[u], 0));
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          o[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (src[u] >= 0 && lane < HD / 4)
+            o[u][i] = load4(rs.part_o + (((size_t)from * (HD / 4) + lane) * R + rrow + i) * 4);
+        }
         todo &= todo - 1;
       }
+    };
+    fetch();
+    float fp[NR];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        acc.a[0] = fmaf(o[u].x, w[u], acc.a[0]);
-        acc.a[1] = fmaf(o[u].y, w[u], acc.a[1]);
-        acc.a[2] = fmaf(o[u].z, w[u], acc.a[2]);
-        acc.a[3] = fmaf(o[u].w, w[u], acc.a[3]);
-      }
+    for (int i = 0; i < NR; ++i) {
+      const float mn = fmaxf(acc[i].m, warp_max(ml[i].x));
+      const float f = acc[i].m == -INFINITY ? 0.f : exp2f(acc[i].m - mn);
+      fp[i] = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - mn);
+      acc[i].l = acc[i].l * f + warp_sum(ml[i].y * fp[i]);
+      acc[i].m = mn;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i].a[k] *= f;
+    }
+    for (;;) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const float w = __shfl_sync(0xffffffffu, fp[i], max(src[u], 0));
+          if (src[u] >= 0) {
+            acc[i].a[0] = fmaf(o[u][i].x, w, acc[i].a[0]);
+            acc[i].a[1] = fmaf(o[u][i].y, w, acc[i].a[1]);
+            acc[i].a[2] = fmaf(o[u][i].z, w, acc[i].a[2]);
+            acc[i].a[3] = fmaf(o[u][i].w, w, acc[i].a[3]);
+          }
+        }
+      if (!todo) break;
+      fetch();
     }
   }
-  return pieces;
 }
 
-// Tree attention, second half: a warp per row joins the pieces over the cache
-// with the node's own ancestors, whose keys it reads one by one -- a chain is
-// short next to the cache, and a product with the whole tree's values would
-// let the infinities of other nodes in (0 x inf).  The rows of 8 warps are
-// neighbours in (node, head), so their chains' rows come from L1.
-// blockIdx.x = (sequence, KV head), blockIdx.y = 8 rows.
+// Tree attention, second half: a warp joins the pieces over the cache with the
+// node's own ancestors, whose keys it reads one by one -- a chain is short next to
+// the cache, and a product with the whole tree's values would let the infinities
+// of other nodes in (0 x inf).  A warp takes NR query heads of one node: they
+// share the chain and its keys, and their sums overlap.
+// blockIdx.x = (sequence, KV head), blockIdx.y = kJoinWarps * NR rows.
 constexpr int kJoinWarps = 8;
-template <typename T, int HD>
+template <typename T, int HD, int NR>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     tree_join_kernel(const __grid_constant__ RowsShape rs, const T* __restrict__ q, const T* __restrict__ kn,
                      const T* __restrict__ vn, const int32_t* __restrict__ parents) {
@@ -694,11 +717,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x / rs.KV, g = blockIdx.x % rs.KV;
   for (int i = threadIdx.x; i < rs.T; i += blockDim.x) par[i] = parents[(size_t)b * rs.T + i];
+  // the plan's loads are on their way together with the parents
+  const RowsTiles<true> tiles_of{rs};
+  const int per = rs.G > 0 ? rs.cuts->per : 0;
+  FlatSeg seg;
+  seg.item = b;
+  seg.n = rs.G > 0 ? tiles_of(b) : 0;
+  int before = 0;
+  for (int i = lane; i < b; i += 32) before += flat_cost(tiles_of(i));
+  before = __reduce_add_sync(0xffffffffu, before);
   __syncthreads();
-  const int r = blockIdx.y * kJoinWarps + warp;     // row t * rep + j
+  const int r = (blockIdx.y * kJoinWarps + warp) * NR;     // row t * rep + j, NR divides rep
   if (r >= rs.T * rs.rep) return;
-  const int t = r / rs.rep, h = g * rs.rep + r % rs.rep;
-  T* o = static_cast<T*>(rs.out) + (((size_t)b * rs.T + t) * rs.H + h) * HD;
+  const int t = r / rs.rep, h = g * rs.rep + r - t * rs.rep;
+  T* o = static_cast<T*>(rs.out) + (((size_t)b * rs.T + t) * rs.H + h) * HD + 4 * lane;
   const bool on = lane < HD / 4;
   // the chain from the node up to its root
   uint8_t* chain = chain_s[warp];
@@ -716,15 +748,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     c = p;
   }
   if (!live) {
-    if (on) store4(o + 4 * lane, 0.f, 0.f, 0.f, 0.f);
+    if (on)
+#pragma unroll
+      for (int i = 0; i < NR; ++i) store4(o + i * HD, 0.f, 0.f, 0.f, 0.f);
     return;
   }
   __syncwarp();
-  // the first four keys of the chain and q are under way while the pieces are joined
-  float4 qv = make_float4(0.f, 0.f, 0.f, 0.f), k[4], v[4];
+  // q and the first keys of the chain are under way while the pieces are joined
+  constexpr int U = 4;
+  float4 qv[NR], k[U], v[U];
   auto fetch = [&](int i0) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < U; ++u) {
       k[u] = v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i0 + u < depth && on) {
         const size_t at = (((size_t)b * rs.T + chain[i0 + u]) * rs.KV + g) * HD + 4 * lane;
@@ -733,73 +768,115 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
       }
     }
   };
-  if (on) qv = load4(q + (((size_t)b * rs.T + t) * rs.H + h) * HD + 4 * lane);
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    qv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) qv[i] = load4(q + (((size_t)b * rs.T + t) * rs.H + h + i) * HD + 4 * lane);
+  }
   fetch(0);
-  RowAcc acc;
-  acc.clear();
-  const RowsTiles<true> tiles_of{rs};
-  FlatSeg seg;
-  seg.item = b;
-  seg.n = rs.G > 0 ? tiles_of(b) : 0;
+  RowAcc acc[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) acc[i].clear();
   if (seg.n > 0) {
     const int mult = tiles_of.mult();
-    const int per = rs.cuts->per;
-    int before = 0;
-    for (int i = lane; i < b; i += 32) before += flat_cost(tiles_of(i));
-    before = __reduce_add_sync(0xffffffffu, before);
     const int rt = t / rs.qpt, grp = rt / rs.slots;
     seg.sub = grp * rs.KV + g;
     seg.s0 = before * mult + seg.sub * flat_cost(seg.n);
-    join_pieces<HD, true>(rs, seg, per, (rt - grp * rs.slots) * rs.tile_rows + r - rt * rs.qpt * rs.rep, acc);
+    join_pieces<HD, NR>(rs, seg, per, (rt - grp * rs.slots) * rs.tile_rows + r - rt * rs.qpt * rs.rep, acc);
   }
-  // four keys at a time, so that their loads and sums overlap
-  for (int i0 = 0; i0 < depth; i0 += 4) {
-    float sc[4];
+  for (int i0 = 0; i0 < depth; i0 += U) {
+    float sc[U][NR];
     if (i0) fetch(i0);
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      sc[u] = fmaf(qv.x, k[u].x, fmaf(qv.y, k[u].y, fmaf(qv.z, k[u].z, qv.w * k[u].w)));
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        sc[u][i] = fmaf(qv[i].x, k[u].x, fmaf(qv[i].y, k[u].y, fmaf(qv[i].z, k[u].z, qv[i].w * k[u].w)));
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sc[u] += __shfl_xor_sync(0xffffffffu, sc[u], s);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (i0 + u < depth) acc.add(sc[u] * rs.scale_log2, 1.f, v[u]);
+        for (int i = 0; i < NR; ++i) sc[u][i] += __shfl_xor_sync(0xffffffffu, sc[u][i], s);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < depth)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) acc[i].add(sc[u][i] * rs.scale_log2, 1.f, v[u]);
   }
-  const float inv = 1.f / acc.l;
-  if (on) store4(o + 4 * lane, acc.a[0] * inv, acc.a[1] * inv, acc.a[2] * inv, acc.a[3] * inv);
+  if (on)
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const float inv = 1.f / acc[i].l;
+      store4(o + i * HD, acc[i].a[0] * inv, acc[i].a[1] * inv, acc[i].a[2] * inv, acc[i].a[3] * inv);
+    }
 }
 
 // Observed attention: the rows of the segments that were cut.  blockIdx.x + 1 is
-// the CTA whose border cuts the segment, blockIdx.y = 16 of its rows.
-constexpr int kCausalJoinRows = 16;
+// the CTA whose border cuts the segment.  The lanes of a warp are 32 neighbouring
+// rows, whose records lie side by side, and a warp takes 16 columns: every load
+// is contiguous, and all pieces' loads are in flight together.
+template <int HD>
+struct CausalJoin {
+  static constexpr int WARPS = HD / 16;                       // for 32 rows
+  static constexpr int ROWS = WARPS >= 4 ? 32 : 128 / WARPS;  // of a block: at least four warps
+  static constexpr int THREADS = WARPS * ROWS;
+};
 template <typename T, int HD>
-__global__ void __launch_bounds__(32 * kJoinWarps) causal_join_kernel(const __grid_constant__ RowsShape rs) {
+__global__ void __launch_bounds__(CausalJoin<HD>::THREADS) causal_join_kernel(const __grid_constant__ RowsShape rs) {
   griddep_wait_and_release();
   const RowsTiles<false> tiles_of{rs};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int per, b, grp, g;
   const FlatSeg seg = flat_cut(rs.cuts, blockIdx.x + 1, per);
   if (seg.n == 0) return;
   tiles_of.where(seg, b, grp, g);
-  const int live = cached_len(rs.seq_lens, b, rs.T);
-  const int first = blockIdx.y * kCausalJoinRows + warp;
-  const int end = min((int)(blockIdx.y + 1) * kCausalJoinRows, rs.slots * rs.tile_rows);
-  for (int r = first; r < end; r += kJoinWarps) {
-    const int rt = grp * rs.slots + r / rs.tile_rows, in = r % rs.tile_rows;
-    const int t_in = in / rs.rep, t = rt * rs.qpt + t_in, h = g * rs.rep + in - t_in * rs.rep;
-    if (t_in >= rs.qpt || t >= live) continue;
-    RowAcc acc;
-    acc.clear();
-    if (join_pieces<HD, false>(rs, seg, per, r, acc) < 2) continue;
-    const float inv = 1.f / acc.l;
-    if (lane < HD / 4)
-      store4(static_cast<T*>(rs.out) + (((size_t)b * rs.T + t) * rs.H + h) * HD + 4 * lane, acc.a[0] * inv,
-             acc.a[1] * inv, acc.a[2] * inv, acc.a[3] * inv);
-    if (lane == 0)
-      rs.nlse[((size_t)(b * rs.KV + g) * rs.tiles + rt) * rs.tile_rows + in] = -(acc.m + log2f(acc.l));
+  const int warp = threadIdx.x >> 5, col = warp % CausalJoin<HD>::WARPS;    // columns 16 col ..
+  const int R = rs.slots * rs.tile_rows;
+  const int r = blockIdx.y * CausalJoin<HD>::ROWS + warp / CausalJoin<HD>::WARPS * 32 + (threadIdx.x & 31);
+  if (r >= R) return;
+  const int rt = grp * rs.slots + r / rs.tile_rows, in = r % rs.tile_rows;
+  const int t_in = in / rs.rep, t = rt * rs.qpt + t_in, h = g * rs.rep + in - t_in * rs.rep;
+  if (t_in >= rs.qpt || t >= cached_len(rs.seq_lens, b, rs.T)) return;
+  const int c0 = seg.s0 / per, c1 = (seg.end() - 1) / per;
+  float m = -INFINITY, l = 0.f, a[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = 0.f;
+  for (int c = c0; c <= c1; c += 2) {        // two pieces in flight
+    float2 ml[2];
+    float4 o[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      int w0, w1;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      if (c + u > c1 || !seg.cut((c + u) * per, (c + u + 1) * per, w0, w1)) continue;
+      if (w0 == 0 && w1 == seg.n) return;    // whole: written by its CTA, no record
+      const size_t id = tiles_of.record(seg, c + u, (c + u) * per);
+      ml[u] = *reinterpret_cast<const float2*>(rs.part_ml + (id * R + r) * 2);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[u][k] = load4(rs.part_o + ((id * (HD / 4) + col * 4 + k) * R + r) * 4);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (ml[u].x == -INFINITY) continue;    // no such piece, or the row saw no key in it
+      const float mn = fmaxf(m, ml[u].x);
+      const float f = m == -INFINITY ? 0.f : exp2f(m - mn), fp = exp2f(ml[u].x - mn);
+      l = l * f + ml[u].y * fp;
+      m = mn;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a[4 * k] = a[4 * k] * f + o[u][k].x * fp;
+        a[4 * k + 1] = a[4 * k + 1] * f + o[u][k].y * fp;
+        a[4 * k + 2] = a[4 * k + 2] * f + o[u][k].z * fp;
+        a[4 * k + 3] = a[4 * k + 3] * f + o[u][k].w * fp;
+      }
+    }
   }
+  const float inv = 1.f / l;
+  T* o = static_cast<T*>(rs.out) + (((size_t)b * rs.T + t) * rs.H + h) * HD + col * 16;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    store4(o + 4 * k, a[4 * k] * inv, a[4 * k + 1] * inv, a[4 * k + 2] * inv, a[4 * k + 3] * inv);
+  if (col == 0) rs.nlse[((size_t)(b * rs.KV + g) * rs.tiles + rt) * rs.tile_rows + in] = -(m + log2f(l));
 }
 
 }  // namespace l3

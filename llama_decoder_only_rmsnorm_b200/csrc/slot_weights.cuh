@@ -70,12 +70,13 @@ struct WeightCfg {
   static constexpr int K_BYTES = CHUNKS * TILE;
   static constexpr int KRING = 3;                        // a segment's two key tiles and the next one's first
   static constexpr int Q_STAGE = CHUNKS * TILE + 1024;   // 128 rows of q and their 128 log-sum-exps
-  static constexpr int RING0 = (232448 - 1024 - 2048 - 1024 - KRING * K_BYTES) / Q_STAGE;
+  static constexpr int RING0 = (232448 - 1024 - 4096 - 1024 - KRING * K_BYTES) / Q_STAGE;
   static constexpr int RING = RING0 > 6 ? 6 : RING0;
   static constexpr int OFF_K = 0;
   static constexpr int OFF_Q = KRING * K_BYTES;
   static constexpr int OFF_SUM = OFF_Q + RING * Q_STAGE;   // [2][key tile][128] sums of the right columns
-  static constexpr int OFF_BAR = OFF_SUM + 2048;
+  static constexpr int OFF_BOX = OFF_SUM + 2048;           // the summing warps' plans, 128 bytes each
+  static constexpr int OFF_BAR = OFF_BOX + 16 * 128;
   static constexpr int N_BARS = 2 * KRING + 2 * RING + 8 + 2;
   static constexpr int SMEM_BYTES = 1024 + OFF_BAR + N_BARS * 8 + 16;
   static_assert(SMEM_BYTES <= 232448 && RING >= 3, "shared memory");
@@ -193,8 +194,9 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     int st = 0, ks = 0;
     uint32_t ph = 0, kph = 0, i = 0;   // i: query tiles so far; buffer i & 1 of each warpgroup
     bool ok = true;
-    while (ok && run.next(tiles_of, seg, w0, w1)) {
+    while (ok && run.next_uniform(tiles_of, seg, w0, w1)) {
       int kst[2];
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!mbar_wait_warp(&k_full[ks], kph, wait_ns)) ok = false;
         kst[h] = ks;
@@ -203,6 +205,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       for (int w = w0; w < w1 && ok; ++w, ++i) {
         if (!mbar_wait_warp(&q_full[st], ph, wait_ns)) { ok = false; break; }
         const uint32_t qa = smem_u32(smem + C::OFF_Q + st * C::Q_STAGE);
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int buf = h * 2 + (i & 1);
           if (!mbar_wait_warp(&s_empty[buf], ((i >> 1) & 1u) ^ 1u, wait_ns)) { ok = false; break; }
@@ -237,16 +240,21 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t s_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + kt * 256 + half * 64;
     float* right = reinterpret_cast<float*>(smem + C::OFF_SUM) + kt * 128 + row;
-    run.start(tiles_of.items(), ws.KV, tiles_of, blockIdx.x, gridDim.x);
+    typedef FlatBox<WeightTiles> Box;
+    static_assert(sizeof(Box) <= 128, "plan");
+    Box* box = reinterpret_cast<Box*>(smem + C::OFF_BOX + (warp - 4) * 128);
+    box->start(tiles_of.items(), ws.KV, tiles_of, blockIdx.x, gridDim.x);
     int st = 0;
     uint32_t i = 0, ph = 0, pieces = 0;
     bool ok = true;
-    while (ok && run.next(tiles_of, seg, w0, w1)) {
-      const int b = seg.item / ws.key_tiles, key0 = (seg.item % ws.key_tiles) * 256 + kt * 128, g = seg.sub;
-      const int key = key0 + row, rt0 = tiles_of.first(seg.item);
+    while (ok && box->next(tiles_of)) {
+      // what the tile loop needs: the first tile's position, and from there what each key sees
+      int b = box->seg.item / ws.key_tiles;
+      const int key0 = (box->seg.item % ws.key_tiles) * 256 + kt * 128;
       const int len = cached_len(ws.kv_lens, b, ws.max_len), live = cached_len(ws.seq_lens, b, ws.S);
+      int left = warp_uniform(box->w1 - box->w0), t0 = (tiles_of.first(box->seg.item) + box->w0) * ws.qpt;
       float sum = 0.f;
-      for (int w = w0; w < w1; ++w, ++i) {
+      for (; left > 0; --left, ++i, t0 += ws.qpt) {
         const int buf = kt * 2 + (i & 1);
         if (!mbar_wait_warp(&q_full[st], ph, wait_ns) || !mbar_wait_warp(&s_full[buf], (i >> 1) & 1u, wait_ns)) {
           ok = false;
@@ -260,12 +268,11 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[buf]);
-        const int t0 = (rt0 + w) * ws.qpt;
         const float* nlse = reinterpret_cast<const float*>(smem + C::OFF_Q + st * C::Q_STAGE + C::CHUNKS * C::TILE);
         float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
         const int hi = min(ws.qpt, live - t0) * ws.rep;
         if (hi < 128 || key0 + 127 > len + t0) {
-          const int lo = max(0, key - len - t0) * ws.rep;
+          const int lo = max(0, key0 + row - len - t0) * ws.rep;
           weight_add<true>(ra, nlse, half * 64, lo, hi, ws.scale_log2, a0, a1);
           weight_add<true>(rb, nlse, half * 64 + 32, lo, hi, ws.scale_log2, a2, a3);
         } else {
@@ -285,10 +292,12 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       if (!mbar_wait_warp(&meet[kt], pieces & 1u, wait_ns)) break;
       if (!half) {
         sum += right[(pieces & 1u) * 256];
-        if (w0 == 0 && w1 == seg.n)
-          put_weight(ws, b, g, key, len, live, sum);
+        seg = box->seg;
+        b = seg.item / ws.key_tiles;
+        if (box->w0 == 0 && box->w1 == seg.n)
+          put_weight(ws, b, seg.sub, key0 + row, len, live, sum);
         else
-          ws.part[(size_t)tiles_of.record(seg, blockIdx.x, run.a) * 256 + kt * 128 + row] = sum;
+          ws.part[(size_t)tiles_of.record(seg, blockIdx.x, box->run.a) * 256 + kt * 128 + row] = sum;
       }
       ++pieces;
     }
