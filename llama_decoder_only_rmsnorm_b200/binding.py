@@ -116,20 +116,23 @@ def header_functions():
 
 # ---------------------------------------------------------------- helpers ---
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return ctypes.c_void_p(t)
-    return ctypes.c_void_p(t.data_ptr())
+    # a plain int: the argument types convert it, and a call has a dozen of them
+    return t if t is None or isinstance(t, int) else t.data_ptr()
+
+
+_raw_stream = None   # torch's current stream as a handle, without building a Stream object (3 us of a call's 8)
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            torch.cuda.current_stream()   # sets CUDA up, or says why it cannot
+            raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            _raw_stream = (lambda: raw(device())) if raw and device else lambda: torch.cuda.current_stream().cuda_stream
+        return _raw_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _check(name, status):

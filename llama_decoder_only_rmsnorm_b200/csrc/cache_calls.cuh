@@ -212,7 +212,7 @@ int run_observe(const llama3_config* c, RowsPlan& p, const ObserveArgs& a, cudaS
   w.cuts = rs.cuts;   // the attention's cuts have been joined when the weights' are written
   if (p.scored) {
     L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
-              launch_k(scored_weights_kernel, dim3((rs.max_len + rs.T + 255) / 256, rs.B * rs.KV), 256, 0, st, w));
+              launch_k(scored_weights_kernel, dim3((rs.max_len + rs.T + 1023) / 1024, rs.B * rs.KV), 256, 0, st, w));
     return launch_check();
   }
   const long long most = (long long)w.B * w.key_tiles * w.KV * w.tiles;
@@ -384,22 +384,26 @@ int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src
   L3_TRY(llama3_evict_workspace_size(cfg, n_layers, batch, max_len, budget, &need));
   if (!ws || ws_bytes < need) return LLAMA3_ERR_WORKSPACE;
   if (!aligned16(ws)) return LLAMA3_ERR_ALIGN;
-  // the kernels count the rows of one launch in 32 bits
-  if ((long long)std::min(n_layers, kEvictLayers) * batch * cfg->n_kv_heads > INT_MAX) return LLAMA3_ERR_ARG;
+  // the kernels count the rows of one launch, and the 16-byte pieces that stay of one layer's sequence, in 32 bits
+  if ((long long)std::min(n_layers, kEvictLayers) * batch * cfg->n_kv_heads > INT_MAX ||
+      (long long)std::min(max_len, budget) * cfg->n_kv_heads * (long long)(cfg->head_dim * esize(cfg) / 16) > INT_MAX / 2)
+    return LLAMA3_ERR_UNSUPPORTED;
   cudaStream_t st = (cudaStream_t)stream;
   const long long words = evict_row_words(max_len, budget);
   EvictParams p;
   memset(&p, 0, sizeof(p));
   p.kv_lens = kv_lens;
   p.positions = positions;
-  p.B = batch; p.KV = cfg->n_kv_heads; p.row16 = (int)(cfg->head_dim * esize(cfg) / 16);
+  p.B = batch; p.KV = cfg->n_kv_heads;
+  p.row16.set((uint32_t)(cfg->head_dim * esize(cfg) / 16));
+  p.slot16.set(p.row16.d * cfg->n_kv_heads);
   p.cap = src_cap; p.dst_cap = dst ? dst_cap : src_cap;
   p.max_len = max_len; p.budget = budget; p.recent = recent; p.in_place = dst ? 0 : 1;
   p.from_words = evict_kept(max_len, budget);
   p.move_words = evict_moves(max_len, budget);
   p.ws_row = words;
-  // as many threads as a row has slots to look at, up to 512
-  const int threads = std::max(64, std::min(512, (max_len / 4 + 31) / 32 * 32));
+  // four slots per thread, up to kEvictThreads of them
+  const int threads = std::max(64, std::min(kEvictThreads, (max_len / 4 + 31) / 32 * 32));
   const bool stored = max_len <= kEvictKeys;
   const int smem = stored ? max_len * 4 : 0;
   static bool done[kMaxDevices];
@@ -418,9 +422,8 @@ int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src
     L3_LAUNCH(LLAMA3_KERNEL_EVICT, st,
               launch_k(stored ? evict_select_kernel<true> : evict_select_kernel<false>, rows, threads, smem, st, p));
     L3_TRY(launch_check());
-    // at least four pieces per thread
-    const long long pieces = (long long)(dst ? p.from_words : p.move_words) * p.row16 * p.KV;
-    const int parts = (int)std::max(1LL, std::min((pieces + 1023) / 1024, 1024LL));
+    const long long pieces = (long long)(dst ? p.from_words : p.move_words) * p.slot16.d;
+    const int parts = (int)std::max(1LL, std::min((pieces + 255) / 256, 65535LL));
     L3_LAUNCH(LLAMA3_KERNEL_EVICT, st, launch_k(evict_move_kernel, dim3(nl * batch, parts), 256, 0, st, p));
     L3_TRY(launch_check());
   }
@@ -472,7 +475,9 @@ int llama3_tree_commit(const llama3_config* cfg, const llama3_bounded_cache* nod
     for (int i = 0; i < nl; ++i)
       p.layer[i] = {(const uint4*)nodes[l0 + i].k, (const uint4*)nodes[l0 + i].v, (uint4*)caches[l0 + i].k,
                     (uint4*)caches[l0 + i].v, caches[l0 + i].weights, caches[l0 + i].slot_pos};
-    L3_LAUNCH(LLAMA3_KERNEL_ACCEPT, st, launch_k(tree_commit_kernel, dim3(batch, nl), 256, 0, st, p));
+    // enough parts for a path of 16 nodes at one piece per thread; longer ones loop
+    const int parts = std::min(std::max(1, (int)(std::min(n_nodes, 16) * (long long)p.row16 / 256)), 64);
+    L3_LAUNCH(LLAMA3_KERNEL_ACCEPT, st, launch_k(tree_commit_kernel, dim3(batch, nl, parts), 256, 0, st, p));
     L3_TRY(launch_check());
   }
   return LLAMA3_OK;

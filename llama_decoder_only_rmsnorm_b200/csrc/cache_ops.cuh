@@ -25,6 +25,25 @@ __device__ __forceinline__ int cached_len(const int32_t* lens, int b, int max_le
 }
 
 // ---- eviction ---------------------------------------------------------------
+// Division of n < 2^31 by a fixed d >= 1 (Granlund and Montgomery, "Division by
+// invariant integers using multiplication"): l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1.
+struct FastDiv {
+  uint32_t d, m;
+  int s1, s2;
+  __host__ void set(uint32_t d_) {
+    d = d_;
+    int l = 0;
+    while (l < 32 && (1ull << l) < d) ++l;
+    m = (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+    s1 = l < 1 ? l : 1;
+    s2 = l < 1 ? 0 : l - 1;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    const uint32_t t = __umulhi(m, n);
+    return (t + ((n - t) >> s1)) >> s2;
+  }
+};
+
 struct EvictLayer {
   const uint4 *k, *v;
   const float* w;
@@ -38,7 +57,8 @@ struct EvictParams {
   EvictLayer layer[kEvictLayers];
   const int32_t *kv_lens, *positions;
   int32_t *ws, *lens_out;
-  int B, KV, row16, cap, dst_cap, max_len, budget, recent, in_place;
+  FastDiv row16, slot16;   // 16-byte pieces of a slot's row of one KV head, and of all
+  int B, KV, cap, dst_cap, max_len, budget, recent, in_place;
   int from_words, move_words;
   long long ws_row;    // words of scratch per row: 4, the sources, the holes and the slots that fill them
 };
@@ -55,7 +75,7 @@ inline long long evict_row_words(int max_len, int budget) {
 
 // Order key of a slot: larger is kept first.  Recent slots come before all
 // others, a NaN weight before every number; -0 equals +0.
-__device__ __forceinline__ uint32_t evict_key(float w, int32_t pos, long long floor_pos) {
+__device__ __forceinline__ uint32_t evict_key(float w, int32_t pos, int32_t floor_pos) {
   if (pos >= floor_pos) return 0xffffffffu;
   if (w != w) return 0xfffffffeu;
   return float_order_key(w == 0.f ? 0.f : w);
@@ -84,18 +104,25 @@ __device__ __forceinline__ void block_scan2(int& x, int& y, int& tx, int& ty, in
 // Order keys of a row that a block keeps in shared memory (128 KB); longer rows
 // compute them anew at every look.
 constexpr int kEvictKeys = 32768;
+// Threads of a block at most, and the keys of each that stay in registers: up to
+// 8192 slots a row, and four blocks on an SM (512 rows are then one wave).
+constexpr int kEvictThreads = 256, kEvictOwn = 32;
+// Keys that one warp searches alone.
+constexpr int kEvictShort = 256;
 
 // One block per (layer, sequence, KV head).  Thread i owns the slots [i * per, (i +
 // 1) * per), so ranks by slot are prefix sums over the threads.  The cut -- the
 // budget-th largest key -- is found two bits at a time by counting: three
-// thresholds per look, counts added up by redux and once through shared
-// memory.  (A radix histogram has most of its increments on a few bins here,
-// since the weights share their exponents: @RADIX@ us against @COUNT@ us for 512 rows
-// of 8192 slots.)  A look whose count is the budget itself ends the search.
+// thresholds per look, counts added up by redux and once through shared memory.
+// What bounds it is the number of instructions (16 looks of a block over 8192
+// keys: 49 us for 512 rows), so once at most 256 keys are left in the interval
+// the search goes on among those, in one warp and without barriers.  A look whose
+// count is the budget itself ends the search.
 template <bool STORED>
-__global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kEvictThreads, 4) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t evict_keys[];
-  __shared__ int scan[64], counts[2][3][16];
+  __shared__ int scan[64], counts[2][3][kEvictThreads / 32], short_n;
+  __shared__ uint32_t short_keys[kEvictShort], short_cut;
   griddep_wait_and_release();
   const int row = blockIdx.x, g = row % p.KV, b = (row / p.KV) % p.B, layer = row / (p.KV * p.B);
   const int NT = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = NT >> 5;
@@ -103,7 +130,7 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant
   const size_t base = ((size_t)b * p.KV + g) * p.cap;
   const float* w = p.layer[layer].w + base;
   const int32_t* pos = p.layer[layer].pos + base;
-  const long long floor_pos = (long long)p.positions[b] - p.recent;
+  const int32_t floor_pos = (int32_t)max((long long)p.positions[b] - p.recent, (long long)INT_MIN);
   int32_t* ws = p.ws + (size_t)row * p.ws_row;
   int32_t* from = ws + 4;                  // source of every kept slot
   int32_t* holes = ws + 4 + p.from_words;
@@ -112,23 +139,31 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant
     for (int i = threadIdx.x; i < left; i += NT) from[i] = i;
     return;
   }
-  // Counting needs no order: up to 16 keys per thread stay in registers for it.
-  uint32_t own[16];
-  const bool in_regs = STORED && n <= 16 * NT;
+  // Counting needs no order: a thread keeps its keys in registers for it.
+  uint32_t own[kEvictOwn];
+  const bool in_regs = STORED && n <= kEvictOwn * NT;
   if (in_regs) {
-    float wv[16];
-    int32_t pv[16];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
-      const int j = threadIdx.x + u * NT;
-      wv[u] = j < n ? w[j] : 0.f;
-      pv[u] = j < n ? pos[j] : 0;
-    }
+    for (int u8 = 0; u8 < kEvictOwn; u8 += 16) {       // sixteen slots' loads in flight
+      if (u8 * NT >= n) {
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
-      const int j = threadIdx.x + u * NT;
-      own[u] = j < n ? evict_key(wv[u], pv[u], floor_pos) : 0u;   // 0 is below every threshold
-      if (j < n) evict_keys[j] = own[u];
+        for (int u = 0; u < 16; ++u) own[u8 + u] = 0u;
+        continue;
+      }
+      float wv[16];
+      int32_t pv[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int j = threadIdx.x + (u8 + u) * NT;
+        wv[u] = j < n ? w[j] : 0.f;
+        pv[u] = j < n ? pos[j] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int j = threadIdx.x + (u8 + u) * NT;
+        own[u8 + u] = j < n ? evict_key(wv[u], pv[u], floor_pos) : 0u;   // 0 is below every threshold
+        if (j < n) evict_keys[j] = own[u8 + u];
+      }
     }
     __syncthreads();
   } else if (STORED) {
@@ -139,16 +174,25 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant
   const int per = ((n + NT - 1) / NT) | 1;
   const int j0 = min(n, (int)threadIdx.x * per), j1 = min(n, j0 + per);
   auto key_at = [&](int j) { return STORED ? evict_keys[j] : evict_key(w[j], pos[j], floor_pos); };
-  uint32_t cut = 0;      // at least `budget` keys are >= cut
-  for (int shift = 30, look = 0; shift >= 0; shift -= 2, look ^= 1) {
-    const uint32_t t1 = cut | (1u << shift), t2 = cut | (2u << shift), t3 = cut | (3u << shift);
+  const int used = in_regs ? (n + NT - 1) / NT : 0;
+  uint32_t cut = 0;              // at_least >= budget keys are >= cut,
+  int at_least = n, over = 0;    // over < budget of them lie behind the open interval [cut, cut + 2^open)
+  int open = 32;
+  bool exact = false;
+  for (int look = 0; open > 0 && !exact && at_least - over > kEvictShort; look ^= 1) {
+    open -= 2;
+    const uint32_t t1 = cut | (1u << open), t2 = cut | (2u << open), t3 = cut | (3u << open);
     int c1 = 0, c2 = 0, c3 = 0;
     if (in_regs) {
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        c1 += own[u] >= t1;
-        c2 += own[u] >= t2;
-        c3 += own[u] >= t3;
+      for (int u4 = 0; u4 < kEvictOwn; u4 += 4) {
+        if (u4 >= used) break;
+#pragma unroll
+        for (int u = u4; u < u4 + 4; ++u) {
+          c1 += own[u] >= t1;
+          c2 += own[u] >= t2;
+          c3 += own[u] >= t3;
+        }
       }
     } else {
       for (int j = j0; j < j1; ++j) {
@@ -166,13 +210,58 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant
     c1 = __reduce_add_sync(0xffffffffu, lane < warps ? counts[look][0][lane] : 0);
     c2 = __reduce_add_sync(0xffffffffu, lane < warps ? counts[look][1][lane] : 0);
     c3 = __reduce_add_sync(0xffffffffu, lane < warps ? counts[look][2][lane] : 0);
-    int found = 0;
-    if (c3 >= p.budget) { cut = t3; found = c3; }
-    else if (c2 >= p.budget) { cut = t2; found = c2; }
-    else if (c1 >= p.budget) { cut = t1; found = c1; }
-    if (found == p.budget) break;
+    if (c3 >= p.budget) { cut = t3; at_least = c3; }
+    else if (c2 >= p.budget) { cut = t2; at_least = c2; over = c3; }
+    else if (c1 >= p.budget) { cut = t1; at_least = c1; over = c2; }
+    else over = c1;
+    exact = at_least == p.budget;
   }
-  // of the slots at the cut the lowest are kept, as many as the budget leaves
+  if (open > 0 && !exact) {
+    // few keys are left in the interval: one warp goes through them, without barriers
+    if (threadIdx.x == 0) short_n = 0;
+    __syncthreads();
+    const uint32_t span = open < 32 ? (1u << open) - 1u : 0xffffffffu;
+    if (in_regs) {
+#pragma unroll
+      for (int u = 0; u < kEvictOwn; ++u)
+        if (threadIdx.x + u * NT < n && own[u] - cut <= span) short_keys[atomicAdd(&short_n, 1)] = own[u];
+    } else {
+      for (int j = j0; j < j1; ++j) {
+        const uint32_t k = key_at(j);
+        if (k - cut <= span) short_keys[atomicAdd(&short_n, 1)] = k;
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int m = short_n, need = p.budget - over;
+      uint32_t mine[kEvictShort / 32];
+#pragma unroll
+      for (int i = 0; i < kEvictShort / 32; ++i) mine[i] = lane + 32 * i < m ? short_keys[lane + 32 * i] : 0u;
+      while (open > 0) {
+        open -= 2;
+        const uint32_t t1 = cut | (1u << open), t2 = cut | (2u << open), t3 = cut | (3u << open);
+        int c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll
+        for (int i = 0; i < kEvictShort / 32; ++i) {
+          c1 += mine[i] >= t1;
+          c2 += mine[i] >= t2;
+          c3 += mine[i] >= t3;
+        }
+        c1 = __reduce_add_sync(0xffffffffu, c1);
+        c2 = __reduce_add_sync(0xffffffffu, c2);
+        c3 = __reduce_add_sync(0xffffffffu, c3);
+        int got = 0;
+        if (c3 >= need) { cut = t3; got = c3; }
+        else if (c2 >= need) { cut = t2; got = c2; }
+        else if (c1 >= need) { cut = t1; got = c1; }
+        if (got == need) break;
+      }
+      if (lane == 0) short_cut = cut;
+    }
+    __syncthreads();
+    cut = short_cut;
+  }
+  // Of the slots at the cut the lowest are kept, as many as the budget leaves.
   int above = 0, equal = 0, all_above, all_equal;
   for (int j = j0; j < j1; ++j) {
     const uint32_t k = key_at(j);
@@ -182,28 +271,39 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant
   const int my_equal = equal;
   block_scan2(above, equal, all_above, all_equal, scan);
   const int room = p.budget - all_above;       // for keys equal to the cut
-  int taken = min(max(room - equal, 0), my_equal);
+  const int taken = min(max(room - equal, 0), my_equal);
+  // The kept ones of up to 32 slots from j on, as bits; eq: how many at the cut are still to be kept.
+  auto kept_bits = [&](int j, int cnt, int& eq) {
+    uint32_t m = 0;
+    for (int i = 0; i < cnt; ++i) {
+      const uint32_t k = key_at(j + i);
+      bool keep = k > cut;
+      if (k == cut && eq > 0) { --eq; keep = true; }
+      m |= (uint32_t)keep << i;
+    }
+    return m;
+  };
+  auto low_bits = [](int cnt) { return cnt <= 0 ? 0u : cnt >= 32 ? 0xffffffffu : (1u << cnt) - 1u; };
   // the evicted slots below the budget and the kept ones behind it
   int n_holes = 0, n_spare = 0, all_holes, all_spare;
-  {
-    int eq = taken;
-    for (int j = j0; j < j1; ++j) {
-      const uint32_t k = key_at(j);
-      const bool keep = k > cut || (k == cut && eq-- > 0);
-      n_holes += j < p.budget && !keep;
-      n_spare += j >= p.budget && keep;
-    }
+  uint32_t bits[2] = {0, 0};       // of the first 64 slots; longer runs look at their keys again
+  for (int j = j0, eq = taken; j < j1; j += 32) {
+    const int cnt = min(32, j1 - j);
+    const uint32_t m = kept_bits(j, cnt, eq), front = low_bits(min(cnt, p.budget - j));
+    n_holes += __popc(~m & front);
+    n_spare += __popc(m & ~front);
+    if (j == j0) bits[0] = m;
+    if (j == j0 + 32) bits[1] = m;
   }
   block_scan2(n_holes, n_spare, all_holes, all_spare, scan);
   int32_t* spare = holes + p.move_words;
-  for (int j = j0; j < j1; ++j) {
-    const uint32_t k = key_at(j);
-    const bool keep = k > cut || (k == cut && taken-- > 0);
-    if (j < p.budget) {
-      if (keep) from[j] = j; else holes[n_holes++] = j;
-    } else if (keep) {
-      spare[n_spare++] = j;
-    }
+  for (int j = j0, eq = taken; j < j1; j += 32) {
+    const int cnt = min(32, j1 - j);
+    const uint32_t front = low_bits(min(cnt, p.budget - j));
+    const uint32_t m = per > 64 ? kept_bits(j, cnt, eq) : j == j0 ? bits[0] : bits[1];
+    for (uint32_t x = m & front; x; x &= x - 1) from[j + __ffs(x) - 1] = j + __ffs(x) - 1;
+    for (uint32_t x = ~m & front; x; x &= x - 1) holes[n_holes++] = j + __ffs(x) - 1;
+    for (uint32_t x = m & ~front; x; x &= x - 1) spare[n_spare++] = j + __ffs(x) - 1;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < all_holes; i += NT) from[holes[i]] = spare[i];
@@ -213,55 +313,41 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const __grid_constant
 // Copies the kept slots: blockIdx.x = (layer, sequence), blockIdx.y = part of its
 // slots.  The KV heads' pieces of one slot lie side by side, so a block takes all
 // heads of its slots and the stores are contiguous although every head keeps other
-// slots.  Four 16-byte pieces of K and of V in flight per thread.  The last launch
-// of a call also writes the lengths: kv_lens_out may be kv_lens, whose shortened
-// values give every block here the same `left`.
-__global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictParams p) {
+// slots.  One 16-byte piece of K and of V per thread and eight blocks on an SM: a
+// copy wants loads in flight, and threads that wait for the look-up of their
+// piece's source stand in each other's way the less, the more there are (8B
+// prompts, 537 MB moved: 145 us with four pieces of each per thread, 120 with two,
+// 109 with one, 145 with one of K or of V).  The last launch of a call also writes
+// the lengths: kv_lens_out may be kv_lens, whose shortened values give every
+// block here the same `left`.
+__global__ void __launch_bounds__(256, 8) evict_move_kernel(const __grid_constant__ EvictParams p) {
   griddep_wait_and_release();
   const int b = blockIdx.x % p.B, layer = blockIdx.x / p.B;
   const EvictLayer& L = p.layer[layer];
   const int len = cached_len(p.kv_lens, b, p.max_len), left = min(len, p.budget);
-  if (p.lens_out && layer == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.lens_out[b] = left;
+  if (p.lens_out && layer == 0 && blockIdx.y + threadIdx.x == 0) p.lens_out[b] = left;
   const int32_t* ws0 = p.ws + (size_t)blockIdx.x * p.KV * p.ws_row;
   // in place: at most as many moves as slots leave, and fewer in some heads
   const int most = p.in_place ? min(len - left, left) : left;
-  const int slot16 = p.row16 * p.KV;
-  const long long total = (long long)most * slot16;
-  const int step = 256 * gridDim.y;
-  for (long long i0 = blockIdx.y * 256 + threadIdx.x; i0 < total; i0 += 4 * step) {
-    uint4 k[4], v[4];
-    int to[4], fr[4], c[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const long long i = i0 + u * step;
-      to[u] = -1;
-      if (i < total) {
-        const int m = (int)(i / slot16);
-        c[u] = (int)(i - (long long)m * slot16);
-        const int32_t* ws = ws0 + (size_t)(c[u] / p.row16) * p.ws_row;
-        to[u] = !p.in_place ? m : m < ws[0] ? ws[4 + p.from_words + m] : -1;
-        if (to[u] >= 0) fr[u] = ws[4 + to[u]];
-      }
+  const uint32_t slot16 = p.slot16.d, total = (uint32_t)most * slot16, step = 256 * gridDim.y;
+  for (uint32_t i = blockIdx.y * 256 + threadIdx.x; i < total; i += step) {
+    const uint32_t m = p.slot16.div(i), c = i - m * slot16, g = p.row16.div(c);
+    const int32_t* ws = ws0 + g * p.ws_row;
+    int to = m;
+    if (p.in_place) {
+      if ((int)m >= __ldg(ws)) continue;
+      to = __ldg(ws + 4 + p.from_words + m);
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (to[u] >= 0) {
-        const size_t at = ((size_t)b * p.cap + fr[u]) * slot16 + c[u];
-        k[u] = L.k[at];
-        v[u] = L.v[at];
-      }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (to[u] >= 0) {
-        const size_t at = ((size_t)b * p.dst_cap + to[u]) * slot16 + c[u];
-        L.dk[at] = k[u];
-        L.dv[at] = v[u];
-        if (c[u] % p.row16 == 0) {
-          const size_t head = (size_t)b * p.KV + c[u] / p.row16;
-          L.dw[head * p.dst_cap + to[u]] = L.w[head * p.cap + fr[u]];
-          L.dpos[head * p.dst_cap + to[u]] = L.pos[head * p.cap + fr[u]];
-        }
-      }
+    const int fr = __ldg(ws + 4 + to);
+    const size_t s = ((size_t)b * p.cap + fr) * slot16 + c, d = ((size_t)b * p.dst_cap + to) * slot16 + c;
+    const uint4 k = L.k[s], v = L.v[s];
+    L.dk[d] = k;
+    L.dv[d] = v;
+    if (c == g * p.row16.d) {
+      const size_t head = (size_t)b * p.KV + g;
+      L.dw[head * p.dst_cap + to] = L.w[head * p.cap + fr];
+      L.dpos[head * p.dst_cap + to] = L.pos[head * p.cap + fr];
+    }
   }
 }
 
@@ -312,7 +398,10 @@ struct CommitParams {
   const int32_t *path, *accepted, *kv_lens, *positions;
   int nodes, KV, row16, cap;   // row16: 16-byte pieces of one token's row (all KV heads)
 };
-// blockIdx.x = sequence, blockIdx.y = layer.
+// blockIdx.x = sequence, blockIdx.y = layer, blockIdx.z = part of the path's rows:
+// one 16-byte piece of K and of V per thread, so that a path costs one round
+// trip however long it is (8B, 32 layers of 8 drafts: 5.3 us, with one block per
+// path 9.1).
 __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant__ CommitParams p) {
   griddep_wait_and_release();
   const int b = blockIdx.x;
@@ -323,17 +412,20 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant_
     if (threadIdx.x == 0) record_error(LLAMA3_ERR_ARG);
     return;
   }
-  for (int i = threadIdx.x; i < n * p.row16; i += 256) {
-    const int m = i / p.row16, c = i % p.row16, from = path[m];
+  const int row = blockIdx.z * 256 + threadIdx.x, step = 256 * gridDim.z;
+  for (long long i = row; i < (long long)n * p.row16; i += step) {
+    const int m = (int)(i / p.row16), c = (int)(i - (long long)m * p.row16), from = path[m];
     if (from < 0 || from >= p.nodes) {
       record_error(LLAMA3_ERR_ARG);
       continue;
     }
     const size_t s = ((size_t)b * p.nodes + from) * p.row16 + c, d = ((size_t)b * p.cap + base + m) * p.row16 + c;
-    L.k[d] = L.kn[s];
-    L.v[d] = L.vn[s];
+    const uint4 k = L.kn[s], v = L.vn[s];
+    L.k[d] = k;
+    L.v[d] = v;
   }
-  for (int i = threadIdx.x; i < n * p.KV; i += 256) {
+  if (!L.w && !L.pos) return;
+  for (int i = row; i < n * p.KV; i += step) {
     const size_t at = ((size_t)b * p.KV + i / n) * p.cap + base + i % n;
     if (L.w) L.w[at] = 0.f;
     if (L.pos) L.pos[at] = (p.positions ? p.positions[b] - n : base) + i % n;

@@ -637,7 +637,7 @@ __device__ __forceinline__ void store4(bf16* p, float a, float b, float c, float
 template <int HD, int NR>
 __device__ __forceinline__ void join_pieces(const RowsShape& rs, const FlatSeg& seg, int per, int rrow,
                                             RowAcc (&acc)[NR]) {
-  constexpr int U = 8 / NR;
+  constexpr int U = NR == 4 ? 2 : 4;
   const RowsTiles<true> tiles_of{rs};
   const int lane = threadIdx.x & 31, R = rs.slots * rs.tile_rows;
   const int c0 = seg.s0 / per, c1 = (seg.end() - 1) / per;
@@ -708,7 +708,7 @@ __device__ __forceinline__ void join_pieces(const RowsShape& rs, const FlatSeg& 
 // blockIdx.x = (sequence, KV head), blockIdx.y = kJoinWarps * NR rows.
 constexpr int kJoinWarps = 8;
 template <typename T, int HD, int NR>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(32 * kJoinWarps, 2)
     tree_join_kernel(const __grid_constant__ RowsShape rs, const T* __restrict__ q, const T* __restrict__ kn,
                      const T* __restrict__ vn, const int32_t* __restrict__ parents) {
   __shared__ int32_t par[kMaxTreeNodes];
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   }
   __syncwarp();
   // q and the first keys of the chain are under way while the pieces are joined
-  constexpr int U = 4;
+  constexpr int U = NR == 4 ? 2 : 4;
   float4 qv[NR], k[U], v[U];
   auto fetch = [&](int i0) {
 #pragma unroll
