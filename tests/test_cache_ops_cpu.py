@@ -150,6 +150,22 @@ def test_acceptance_refuses_bad_arguments():
         B.llama3_tree_commit(c, _caches(2), _caches(1), 64, 2, 8, None, None, None)
 
 
+def test_what_no_kernel_takes_is_refused():
+    unsupported = 7
+    wide = B.make_config(65 * 16, 65, 1, 64, dtype="f32")       # more query heads per KV head than a tile has rows
+    wide16 = B.make_config(129 * 64, 129, 1, 64)
+    for c in (wide, wide16):
+        for size in (lambda: B.llama3_tree_workspace_size(c, 1, 4, 10), lambda: B.llama3_observe_workspace_size(c, 1, 4, 10)):
+            with pytest.raises(B.Llama3Error) as e:
+                size()
+            assert e.value.status == unsupported
+    with pytest.raises(B.Llama3Error) as e:     # more pieces of work than the plan counts
+        B.llama3_observe_workspace_size(cfg(), 8, 1 << 20, 0)
+    assert e.value.status == unsupported
+    assert B.llama3_tree_workspace_size(B.make_config(128 * 64, 128, 1, 64), 1, 4, 10) > 0
+    assert B.llama3_tree_workspace_size(cfg(), 1, 4, 0) == 0    # nothing cached: nothing to keep
+
+
 def test_tree_oracle_of_a_chain_is_causal_attention():
     rng = np.random.default_rng(3)
     q, k, v = (rng.standard_normal((1, n, h, 8)) for n, h in ((5, 4), (12, 2), (12, 2)))

@@ -138,6 +138,15 @@ def test_tree_attention_sizes(hd, dtype, T, shape, lens, max_len):
     run_tree(4, 2, hd, dtype, lens, T, par, seed=T + hd, max_len=max_len)
 
 
+@pytest.mark.parametrize("H,KV,hd,dtype", [(100, 1, 32, "bf16"), (64, 1, 16, "f32"), (33, 1, 96, "bf16"),
+                                           (128, 1, 128, "bf16")])
+def test_many_heads_of_one_kv_head(H, KV, hd, dtype):
+    par = make_tree(np.random.default_rng(9), 3, "random")[None]
+    run_tree(H, KV, hd, dtype, [140], 3, par)
+    run_observe(H, KV, hd, dtype, [140], 3, [2])
+    run_observe(H, KV, hd, dtype, [140], 1, [1])
+
+
 def test_tree_attention_long_cache_is_split():
     par = make_tree(np.random.default_rng(1), 5, "random")[None]
     run_tree(4, 1, 128, "bf16", [20011], 5, par)
@@ -440,3 +449,309 @@ def test_commit_leaves_a_full_cache_alone():
                          i32([3]), i32([3]))   # nodes that do not exist are skipped
     assert caches[0]["k"][0, 0].all() and not caches[0]["k"][0, 1:].any()
     STATUS = 1
+
+
+# ------------------------------------------------------------ ways of calling
+def _tree_call(seed, lens=(300, 17), T=12, H=8, KV=2, hd=128):
+    """A tree attention call and its output: call(stream)."""
+    rng = np.random.default_rng(seed)
+    Bn, max_len = len(lens), max(lens)
+    par = i32(np.stack([make_tree(rng, T, "random") for _ in lens]))
+    q, kn, vn = (randn(rng, (Bn, T, h, hd), "bf16").to(DEV) for h in (H, KV, KV))
+    k, v = (randn(rng, (Bn, max_len, KV, hd), "bf16").to(DEV) for _ in range(2))
+    cfg, d_lens = conf(H, KV, hd, "bf16"), i32(lens)
+    ws = workspace(B.llama3_tree_workspace_size(cfg, Bn, T, max_len))
+    out = G.zeros((Bn, T, H * hd), torch.bfloat16)
+    return lambda stream=None: B.llama3_attention_tree(cfg, q, k, v, max_len, d_lens, max_len, kn, vn, par, Bn, T, out,
+                                                       ws, ws.numel(), stream), out
+
+
+def _observe_call(seed, S, lens=(300, 17), H=8, KV=2, hd=128):
+    rng = np.random.default_rng(seed)
+    Bn, max_len = len(lens), max(lens)
+    cap = max_len + S
+    q = randn(rng, (Bn, S, H, hd), "bf16").to(DEV)
+    k, v = (randn(rng, (Bn, cap, KV, hd), "bf16").to(DEV) for _ in range(2))
+    cfg, d_lens = conf(H, KV, hd, "bf16"), i32(lens)
+    ws = workspace(B.llama3_observe_workspace_size(cfg, Bn, S, max_len))
+    out, w = G.zeros((Bn, S, H * hd), torch.bfloat16), G.zeros((Bn, KV, cap))
+    return lambda stream=None: B.llama3_attention_observed(cfg, q, k, v, cap, Bn, S, d_lens, None, max_len, out, None, w,
+                                                           None, None, ws, ws.numel(), stream), (out, w)
+
+
+def test_two_streams_at_once_give_what_one_gives():
+    calls = [_tree_call(1), _observe_call(2, 1), _tree_call(3, (1000,), 64), _observe_call(4, 150)]
+    for call, _ in calls:
+        call()
+    torch.cuda.synchronize()
+    flat = lambda o: [t.clone() for t in (o if isinstance(o, tuple) else (o,))]
+    want = [flat(o) for _, o in calls]
+    for _, o in calls:
+        for t in (o if isinstance(o, tuple) else (o,)):
+            t.zero_()
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (call, _), s in zip(calls, streams):
+            call(s)
+    torch.cuda.synchronize()
+    for (_, o), w in zip(calls, want):
+        for a, b in zip(flat(o), w):
+            assert torch.equal(a, b)
+
+
+def test_ordinary_launches_give_the_same():
+    for make in (lambda: _tree_call(5), lambda: _observe_call(6, 1), lambda: _observe_call(7, 70)):
+        call, o = make()
+        call()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (o if isinstance(o, tuple) else (o,))]
+        old = B.llama3_set_programmatic_launch(0)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            B.llama3_set_programmatic_launch(old)
+        assert all(torch.equal(a, b) for a, b in zip(o if isinstance(o, tuple) else (o,), want))
+
+
+def test_rows_far_behind_4_gib():
+    # the last sequence's rows begin 8 GiB into each cache, and the capacity bounds every plan
+    H, KV, hd, cap, Bn, n = 8, 8, 128, 1 << 20, 5, 90
+    rng = np.random.default_rng(11)
+    k, v = (torch.zeros((Bn, cap, KV, hd), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    rows = [randn(rng, (n + 8, KV, hd), "bf16") for _ in range(2)]
+    k[-1, :n + 8], v[-1, :n + 8] = rows[0].to(DEV), rows[1].to(DEV)
+    lens = [0] * (Bn - 1) + [n]
+    cfg, d_lens, T = conf(H, KV, hd, "bf16"), i32(lens), 4
+    par = np.tile(make_tree(rng, T, "chain"), (Bn, 1))
+    q = randn(rng, (Bn, T, H, hd), "bf16")
+    kn, vn = (randn(rng, (Bn, T, KV, hd), "bf16") for _ in range(2))
+    max_len = cap - T
+    ws = workspace(B.llama3_tree_workspace_size(cfg, Bn, T, max_len))
+    out = G.zeros((Bn, T, H * hd), torch.bfloat16)
+    B.llama3_attention_tree(cfg, q.to(DEV), k, v, cap, d_lens, max_len, kn.to(DEV), vn.to(DEV), i32(par), Bn, T, out, ws,
+                            ws.numel())
+    want, mag, dot = C.tree_attention(f64(q[-1:]), f64(rows[0][None]), f64(rows[1][None]), [n], f64(kn[-1:]),
+                                      f64(vn[-1:]), par[-1:])
+    check(f64(out[-1]).reshape(want[0].shape), want[0], out_bound(want, mag, dot, hd, n + T, "bf16")[0], "tree")
+    for S in (1, T):
+        ws = workspace(B.llama3_observe_workspace_size(cfg, Bn, S, max_len))
+        w = torch.zeros((Bn, KV, cap), device=DEV)
+        out = G.zeros((Bn, S, H * hd), torch.bfloat16)
+        live = [0] * (Bn - 1) + [S]
+        B.llama3_attention_observed(cfg, q[:, :S].contiguous().to(DEV), k, v, cap, Bn, S, d_lens, i32(live), max_len,
+                                    out, None, w, None, None, ws, ws.numel())
+        want, mag, dot, wts = C.observed_attention(f64(q[-1:, :S]), f64(rows[0][None]), f64(rows[1][None]), [n], [S],
+                                                   None)
+        check(f64(out[-1]).reshape(want[0].shape), want[0], out_bound(want, mag, dot, hd, n + S, "bf16")[0], "out")
+        np.testing.assert_allclose(f64(w[-1, :, :n + S]), wts[0, :, :n + S], rtol=2e-5, atol=1e-9)
+        assert not w[-1, :, n + S:].any() and not w[:-1].any()
+    # eviction of the last sequence into its own place, and a path committed behind it
+    w = torch.zeros((Bn, KV, cap), device=DEV)
+    pos = torch.zeros((Bn, KV, cap), dtype=torch.int32, device=DEV)
+    wr = rng.uniform(0, 1, (KV, n)).astype(np.float32)
+    w[-1, :, :n], pos[-1, :, :n] = torch.from_numpy(wr).to(DEV), torch.arange(n, dtype=torch.int32, device=DEV)
+    cache = B.make_bounded_caches([dict(k=k, v=v, weights=w, slot_pos=pos)])
+    budget, recent, d_pos = 40, 10, i32([n] * Bn)
+    ws = workspace(B.llama3_evict_workspace_size(cfg, 1, Bn, cap, budget))
+    B.llama3_cache_evict(cfg, cache, cap, None, 0, Bn, d_lens, cap, budget, recent, d_pos, d_lens, ws, ws.numel())
+    assert d_lens.tolist() == [0] * (Bn - 1) + [budget]
+    for g in range(KV):
+        take = C.evict_sources(wr[g], np.arange(n), n, n, budget, recent)
+        assert torch.equal(k[-1, :budget, g].cpu(), rows[0][take, g]) and torch.equal(v[-1, :budget, g].cpu(), rows[1][take, g])
+        assert pos[-1, g, :budget].tolist() == take
+    nodes = B.make_bounded_caches([dict(k=kn.to(DEV), v=vn.to(DEV))])
+    keep = nodes, kn.to(DEV), vn.to(DEV)
+    nodes = B.make_bounded_caches([dict(k=keep[1], v=keep[2])])
+    d_lens += 2
+    B.llama3_tree_commit(cfg, nodes, cache, cap, Bn, T, i32([[0, 2, -1, -1]] * Bn), i32([2] * Bn), d_lens)
+    assert torch.equal(k[-1, budget:budget + 2].cpu(), kn[-1, [0, 2]]) and torch.equal(v[0, :2].cpu(), vn[0, [0, 2]])
+
+
+# ----------------------------------------------------- all of them, as they are used
+class Bounded:
+    """Two layers of bounded caches driven as a drafting, evicting decoder drives
+    them; what the model's projections would give is drawn at random."""
+    H, KV, HD, L, BN, CAP, T = 8, 2, 64, 2, 3, 96, 9
+
+    def __init__(self, dtype, seed):
+        self.rng, self.dtype = np.random.default_rng(seed), dtype
+        self.cfg = conf(self.H, self.KV, self.HD, dtype)
+        shape = (self.BN, self.CAP, self.KV, self.HD)
+        self.layers = [dict(k=G.full(shape, float("nan"), dt(dtype)), v=G.full(shape, float("nan"), dt(dtype)),
+                            weights=G.full((self.BN, self.KV, self.CAP), float("nan")),
+                            slot_pos=G.full((self.BN, self.KV, self.CAP), -1, torch.int32)) for _ in range(self.L)]
+        self.caches = B.make_bounded_caches(self.layers)
+        self.lens, self.pos = G.zeros((self.BN,), torch.int32), G.zeros((self.BN,), torch.int32)
+        cfg = self.cfg
+        n = max(B.llama3_observe_workspace_size(cfg, self.BN, 40, self.CAP - 40),
+                B.llama3_observe_workspace_size(cfg, self.BN, 1, self.CAP - 1),
+                B.llama3_tree_workspace_size(cfg, self.BN, self.T, self.CAP),
+                B.llama3_evict_workspace_size(cfg, self.L, self.BN, self.CAP, 24))
+        self.ws = workspace(n)
+
+    def draw(self, S):
+        return [[randn(self.rng, (self.BN, S, h, self.HD), self.dtype).to(DEV) for h in (self.H, self.KV, self.KV)]
+                for _ in range(self.L)]
+
+    def observe(self, qkv, rows, out):
+        S = qkv[0][0].shape[1]
+        lens = self.lens.tolist()
+        for (q, k, v), c, o in zip(qkv, self.layers, out):
+            for b in range(self.BN):
+                c["k"][b, lens[b]:lens[b] + rows[b]] = k[b, :rows[b]]
+                c["v"][b, lens[b]:lens[b] + rows[b]] = v[b, :rows[b]]
+            B.llama3_attention_observed(self.cfg, q, c["k"], c["v"], self.CAP, self.BN, S, self.lens, i32(rows),
+                                        self.CAP - S, o, c["weights"], c["weights"], self.pos, c["slot_pos"], self.ws,
+                                        self.ws.numel())
+        self.lens += i32(rows)
+        self.pos += i32(rows)
+
+    def evict(self, budget, recent):
+        B.llama3_cache_evict(self.cfg, self.caches, self.CAP, None, 0, self.BN, self.lens, self.CAP, budget, recent,
+                             self.pos, self.lens, self.ws, self.ws.numel())
+
+    def tree(self, qkv, par, out):
+        for (q, k, v), c, o in zip(qkv, self.layers, out):
+            B.llama3_attention_tree(self.cfg, q, c["k"], c["v"], self.CAP, self.lens, self.CAP, k, v, par, self.BN,
+                                    self.T, o, self.ws, self.ws.numel())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_drafting_decoder_with_bounded_caches(dtype):
+    m = Bounded(dtype, 21)
+    KV, BN, T = m.KV, m.BN, m.T
+    out_t = lambda S: [G.zeros((BN, S, m.H * m.HD), dt(dtype)) for _ in range(m.L)]
+    mirror = [[dict(k=[], v=[], pos=[[] for _ in range(KV)]) for _ in range(BN)] for _ in range(m.L)]   # rows per head
+    seen = [0] * BN
+
+    def rows_of(l, b):   # the mirror as [1, n, KV, hd]
+        c = mirror[l][b]
+        pack = lambda x: np.stack([np.stack(r) for r in x])[None] if x else np.zeros((1, 0, KV, m.HD))
+        return pack(c["k"]), pack(c["v"])
+
+    def step_observe(S, rows):
+        qkv, out = m.draw(S), out_t(S)
+        before = [f64(c["weights"]) for c in m.layers]
+        lens = [len(mirror[0][b]["k"]) for b in range(BN)]
+        m.observe(qkv, rows, out)
+        for l, (q, k, v) in enumerate(qkv):
+            for b in range(BN):
+                for t in range(rows[b]):
+                    mirror[l][b]["k"].append(f64(k[b, t]))
+                    mirror[l][b]["v"].append(f64(v[b, t]))
+                    for g in range(KV):
+                        mirror[l][b]["pos"][g].append(seen[b] + t)
+                kk, vv = rows_of(l, b)
+                want, mag, dot, w = C.observed_attention(f64(q[b:b + 1]), kk, vv, [lens[b]], [rows[b]],
+                                                         before[l][b:b + 1, :, :kk.shape[1]])
+                check(f64(out[l][b]).reshape(want[0].shape), want[0],
+                      out_bound(want, mag, dot, m.HD, kk.shape[1], dtype)[0], "out")
+                np.testing.assert_allclose(f64(m.layers[l]["weights"][b, :, :kk.shape[1]]), w[0], rtol=2e-5, atol=1e-7)
+        for b in range(BN):
+            seen[b] += rows[b]
+
+    def step_evict(budget, recent):
+        lens = [len(mirror[0][b]["k"]) for b in range(BN)]
+        weights = [c["weights"].cpu().numpy() for c in m.layers]   # the device's own sums decide
+        m.evict(budget, recent)
+        for l in range(m.L):
+            for b in range(BN):
+                c, n = mirror[l][b], min(lens[b], budget)
+                new_k, new_v = [np.zeros((KV, m.HD)) for _ in range(n)], [np.zeros((KV, m.HD)) for _ in range(n)]
+                for g in range(KV):
+                    take = C.evict_sources(weights[l][b, g], c["pos"][g], lens[b], seen[b], budget, recent)
+                    for i, j in enumerate(take):
+                        new_k[i][g], new_v[i][g] = c["k"][j][g], c["v"][j][g]
+                    c["pos"][g] = [c["pos"][g][j] for j in take]
+                c["k"], c["v"] = new_k, new_v
+
+    def step_tree(live):
+        qkv, out = m.draw(T), out_t(T)
+        par = np.stack([make_tree(m.rng, T, "random", n) for n in live])
+        m.tree(qkv, i32(par), out)
+        draft, target = m.rng.integers(0, 3, (BN, T)), m.rng.integers(0, 3, (BN, T))
+        path, acc, nxt = (G.zeros(s, torch.int32) for s in ((BN, T), (BN,), (BN,)))
+        B.llama3_tree_accept(i32(draft), i32(target), i32(par), BN, T, m.lens, path, acc, nxt, m.lens, m.pos, m.pos)
+        nodes = B.make_bounded_caches([dict(k=k, v=v) for _, k, v in qkv])
+        B.llama3_tree_commit(m.cfg, nodes, m.caches, m.CAP, BN, T, path, acc, m.lens, m.pos)
+        for b in range(BN):
+            p, token = C.accept(draft[b], target[b], par[b])
+            assert path[b, :len(p)].tolist() == p and nxt[b].item() == token
+            for l, (q, k, v) in enumerate(qkv):
+                kk, vv = rows_of(l, b)
+                want, mag, dot = C.tree_attention(f64(q[b:b + 1]), kk, vv, [kk.shape[1]], f64(k[b:b + 1]), f64(v[b:b + 1]),
+                                                  par[b:b + 1])
+                check(f64(out[l][b]).reshape(want[0].shape), want[0],
+                      out_bound(want, mag, dot, m.HD, kk.shape[1] + T, dtype)[0], "tree")
+                for i, t in enumerate(p):
+                    mirror[l][b]["k"].append(f64(k[b, t]))
+                    mirror[l][b]["v"].append(f64(v[b, t]))
+                    for g in range(KV):
+                        mirror[l][b]["pos"][g].append(seen[b] + i)
+            seen[b] += len(p)
+
+    step_observe(40, [40, 23, 31])      # padded prompts
+    step_evict(24, 6)
+    for live in ([9, 4, 0], [9, 9, 7]):
+        step_tree(live)
+        step_observe(1, [1, 1, 0])
+    step_evict(24, 6)
+    step_observe(1, [1, 1, 1])
+    for l, c in enumerate(m.layers):
+        for b in range(BN):
+            n = len(mirror[l][b]["k"])
+            assert m.lens[b].item() == n and m.pos[b].item() == seen[b]
+            np.testing.assert_array_equal(f64(c["k"][b, :n]), rows_of(l, b)[0][0])
+            np.testing.assert_array_equal(f64(c["v"][b, :n]), rows_of(l, b)[1][0])
+            for g in range(KV):
+                assert c["slot_pos"][b, g, :n].tolist() == mirror[l][b]["pos"][g]
+            assert torch.isfinite(c["weights"][b, :, :n]).all()
+
+
+def test_a_verification_step_replays_from_a_graph():
+    # one captured step (tree attention, acceptance, commit, eviction), replayed as the caches grow and shrink
+    def steps(m, graph):
+        qkv = m.draw(m.T)
+        par = i32(np.stack([make_tree(m.rng, m.T, "random", n) for n in (9, 7, 9)]))
+        draft, target = (i32(m.rng.integers(0, 2, (m.BN, m.T))) for _ in range(2))
+        path, acc, nxt = (G.zeros(s, torch.int32) for s in ((m.BN, m.T), (m.BN,), (m.BN,)))
+        out = [G.zeros((m.BN, m.T, m.H * m.HD), torch.bfloat16) for _ in range(m.L)]
+        nodes = B.make_bounded_caches([dict(k=k, v=v) for _, k, v in qkv])
+
+        def one():
+            m.tree(qkv, par, out)
+            B.llama3_tree_accept(draft, target, par, m.BN, m.T, m.lens, path, acc, nxt, m.lens, m.pos, m.pos)
+            B.llama3_tree_commit(m.cfg, nodes, m.caches, m.CAP, m.BN, m.T, path, acc, m.lens, m.pos)
+            m.evict(24, 6)
+
+        results = []
+        if graph:
+            state = [t.clone() for c in m.layers for t in c.values()] + [m.lens.clone(), m.pos.clone()]
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                one()
+            torch.cuda.current_stream().wait_stream(side)
+            for t, old in zip([t for c in m.layers for t in c.values()] + [m.lens, m.pos], state):
+                t.copy_(old)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                one()
+        for _ in range(5):
+            g.replay() if graph else one()
+            torch.cuda.synchronize()
+            results.append([t.clone() for t in out + [path, acc, nxt, m.lens, m.pos]])
+        results.append([c[n][b, :x] if n in "kv" else c[n][b, :, :x] for c in m.layers for n in c
+                        for b, x in enumerate(m.lens.tolist())])
+        return results
+
+    runs = []
+    for graph in (False, True):
+        m = Bounded("bf16", 33)
+        m.observe(m.draw(40), [40, 23, 31], [G.zeros((m.BN, 40, m.H * m.HD), torch.bfloat16) for _ in range(m.L)])
+        m.evict(24, 6)
+        runs.append(steps(m, graph))
+    for a, b in zip(*runs):
+        assert len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
