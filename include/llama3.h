@@ -388,9 +388,12 @@ int llama3_tree_workspace_size(const llama3_config* cfg, int batch, int n_nodes,
  * bound the caller knows without reading it.  out: [batch, n_nodes, H*hd];
  * rows of padding nodes are written as zeros.
  * ws: at least llama3_tree_workspace_size(cfg, batch, n_nodes, max_len) bytes.
+ * Calls that may run at the same time need workspaces of their own.
  * Errors: LLAMA3_ERR_ARG (null pointers, n_nodes outside [1, 256], max_len
  * outside [0, cache_cap], ...), LLAMA3_ERR_ALIGN (kv_lens and parents 4-byte,
- * all others 16-byte aligned), LLAMA3_ERR_WORKSPACE, LLAMA3_ERR_CUDA.
+ * all others 16-byte aligned), LLAMA3_ERR_UNSUPPORTED (more query heads per KV
+ * head than 128 for bf16 with head_dim >= 32, than 64 otherwise; more than
+ * 2^30 tiles of work), LLAMA3_ERR_WORKSPACE, LLAMA3_ERR_CUDA.
  */
 int llama3_attention_tree(const llama3_config* cfg, const void* q, const void* k_cache, const void* v_cache,
                           int cache_cap, const int32_t* kv_lens, int max_len, const void* k_nodes,
@@ -440,7 +443,9 @@ typedef struct llama3_bounded_cache {
  * slots start with weight 0 and with the positions
  * positions[b] - n_accepted[b] + i (positions as llama3_tree_accept left it;
  * NULL: the cache row itself).  A sequence whose rows do not fit the cache is
- * left alone and reported as LLAMA3_ERR_ARG through llama3_device_status.
+ * left alone and reported as LLAMA3_ERR_ARG through llama3_device_status (so is
+ * a path entry outside [0, n_nodes), whose row is left out).  The nodes' buffers
+ * must not overlap the caches.
  * Errors: LLAMA3_ERR_ARG, LLAMA3_ERR_ALIGN, LLAMA3_ERR_CUDA.
  */
 int llama3_tree_commit(const llama3_config* cfg, const llama3_bounded_cache* nodes,
@@ -475,10 +480,15 @@ int llama3_observe_workspace_size(const llama3_config* cfg, int batch, int seq, 
  * out and no weight.  Values outside are clamped and reported as
  * LLAMA3_ERR_ARG through llama3_device_status.  slot_pos (nullable): the
  * chunk's slots get positions[b] + t (positions NULL: kv_lens[b] + t).
- * The sums have a fixed order: equal inputs give equal bits.
- * ws: llama3_observe_workspace_size(cfg, batch, seq, max_len) bytes.
+ * Cache rows behind kv_lens[b] + seq_lens[b] and padding rows of q have no
+ * influence, whatever they hold.  The chunk's live rows are expected to be
+ * finite: an infinity or a NaN in one may reach the outputs of rows before it.
+ * The sums have a fixed order: equal inputs give equal bits on one kind of GPU.
+ * ws: llama3_observe_workspace_size(cfg, batch, seq, max_len) bytes; calls that
+ * may run at the same time need workspaces of their own.
  * Errors: LLAMA3_ERR_ARG, LLAMA3_ERR_ALIGN (the int32 and float arrays 4-byte,
- * all others 16-byte aligned), LLAMA3_ERR_WORKSPACE, LLAMA3_ERR_CUDA.
+ * all others 16-byte aligned), LLAMA3_ERR_UNSUPPORTED (as llama3_attention_tree),
+ * LLAMA3_ERR_WORKSPACE, LLAMA3_ERR_CUDA.
  */
 int llama3_attention_observed(const llama3_config* cfg, const void* q, const void* k_cache,
                               const void* v_cache, int cache_cap, int batch, int seq, const int32_t* kv_lens,
@@ -507,7 +517,8 @@ int llama3_evict_workspace_size(const llama3_config* cfg, int n_layers, int batc
  * positions: device int32 [batch]; kv_lens in [0, max_len] (clamped and
  * reported as LLAMA3_ERR_ARG through llama3_device_status otherwise).
  * Errors: LLAMA3_ERR_ARG (recent outside [0, budget], ...), LLAMA3_ERR_ALIGN,
- * LLAMA3_ERR_WORKSPACE, LLAMA3_ERR_CUDA.
+ * LLAMA3_ERR_UNSUPPORTED (2^30 and more 16-byte pieces of K to keep per layer
+ * and sequence), LLAMA3_ERR_WORKSPACE, LLAMA3_ERR_CUDA.
  */
 int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src, int src_cap,
                        const llama3_bounded_cache* dst, int dst_cap, int n_layers, int batch,

@@ -324,11 +324,12 @@ __global__ void __launch_bounds__(256, 8) evict_move_kernel(const __grid_constan
   griddep_wait_and_release();
   const int b = blockIdx.x % p.B, layer = blockIdx.x / p.B;
   const EvictLayer& L = p.layer[layer];
-  const int len = cached_len(p.kv_lens, b, p.max_len), left = min(len, p.budget);
+  const int left = min(cached_len(p.kv_lens, b, p.max_len), p.budget);
   if (p.lens_out && layer == 0 && blockIdx.y + threadIdx.x == 0) p.lens_out[b] = left;
   const int32_t* ws0 = p.ws + (size_t)blockIdx.x * p.KV * p.ws_row;
-  // in place: at most as many moves as slots leave, and fewer in some heads
-  const int most = p.in_place ? min(len - left, left) : left;
+  // In place each head has its own number of moves, at most move_words: a bound
+  // from the lengths would change under the blocks once they are shortened.
+  const int most = p.in_place ? min(p.move_words, left) : left;
   const uint32_t slot16 = p.slot16.d, total = (uint32_t)most * slot16, step = 256 * gridDim.y;
   for (uint32_t i = blockIdx.y * 256 + threadIdx.x; i < total; i += step) {
     const uint32_t m = p.slot16.div(i), c = i - m * slot16, g = p.row16.div(c);

@@ -138,9 +138,12 @@ struct FlatRun {
       } else if (++seg.sub == mult) {
         seg.sub = 0;
         do {
-          ++seg.item;
+          if (++seg.item == items) {   // never reached while units below e <= total are left
+            more = false;
+            break;
+          }
           seg.n = n_of(seg.item);
-        } while (seg.n == 0);   // ends: units below e <= total are left
+        } while (seg.n == 0);
       }
       if (some) return true;
     }

@@ -374,6 +374,11 @@ def test_eviction_many_layers_and_long_rows():
     run_evict(1, 1, 16, "f32", [70001], 70001, 300, 50, True)
 
 
+def test_eviction_in_place_shortens_the_lengths_it_reads():
+    # more blocks than run at once, and kv_lens_out is kv_lens: those that start late see the new lengths
+    run_evict(32, 2, 128, "bf16", [2048, 1900], 2048, 700, 100, True)
+
+
 def test_eviction_into_a_smaller_cache_than_the_budget():
     run_evict(1, 2, 64, "bf16", [20, 7], 20, 64, 9, False, max_len=20)
 
