@@ -404,12 +404,17 @@ int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src
   p.from_words = evict_kept(max_len, budget);
   p.move_words = evict_moves(max_len, budget);
   p.ws_row = words;
-  // four slots per thread, up to kEvictThreads of them
-  const int threads = std::max(64, std::min(kEvictThreads, (max_len / 4 + 31) / 32 * 32));
+  const bool many = (long long)std::min(n_layers, kEvictLayers) * batch * cfg->n_kv_heads >= 2LL * num_sms() &&
+                    max_len <= EvictCfg<true>::THREADS * EvictCfg<true>::OWN;
   const bool stored = max_len <= kEvictKeys;
+  auto select = stored ? (many ? evict_select_kernel<true, true> : evict_select_kernel<true, false>)
+                       : (many ? evict_select_kernel<false, true> : evict_select_kernel<false, false>);
+  // four slots per thread, up to the kernel's threads
+  const int most_threads = many ? EvictCfg<true>::THREADS : EvictCfg<false>::THREADS;
+  const int threads = std::max(64, std::min(most_threads, (int)(((long long)max_len / 4 + 31) / 32 * 32)));
   const int smem = stored ? max_len * 4 : 0;
-  static bool done[kMaxDevices];
-  L3_TRY(opt_in_smem(evict_select_kernel<true>, kEvictKeys * 4, done));
+  static bool done[2][kMaxDevices];
+  if (stored) L3_TRY(opt_in_smem(select, kEvictKeys * 4, done[many]));
   for (int l0 = 0; l0 < n_layers; l0 += kEvictLayers) {
     const int nl = std::min(kEvictLayers, n_layers - l0);
     for (int i = 0; i < nl; ++i) {
@@ -422,7 +427,7 @@ int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src
     const int rows = nl * batch * cfg->n_kv_heads;
     p.lens_out = l0 + nl == n_layers ? kv_lens_out : nullptr;
     L3_LAUNCH(LLAMA3_KERNEL_EVICT, st,
-              launch_k(stored ? evict_select_kernel<true> : evict_select_kernel<false>, rows, threads, smem, st, p));
+              launch_k(select, rows, threads, smem, st, p));
     L3_TRY(launch_check());
     const long long pieces = (long long)(dst ? p.from_words : p.move_words) * p.slot16.d;
     const int parts = (int)std::max(1LL, std::min((pieces + 255) / 256, 65535LL));

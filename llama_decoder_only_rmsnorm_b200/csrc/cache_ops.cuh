@@ -104,9 +104,14 @@ __device__ __forceinline__ void block_scan2(int& x, int& y, int& tx, int& ty, in
 // Order keys of a row that a block keeps in shared memory (128 KB); longer rows
 // compute them anew at every look.
 constexpr int kEvictKeys = 32768;
-// Threads of a block at most, and the keys of each that stay in registers: up to
-// 8192 slots a row, and four blocks on an SM (512 rows are then one wave).
-constexpr int kEvictThreads = 256, kEvictOwn = 32;
+// Threads of a block at most, and the keys of each that stay in registers.  Many
+// rows: 256 threads of 32 keys, four blocks on an SM (512 rows are then one wave).
+// Fewer rows than two per SM, or more slots than that: 1024 threads of 16 keys
+// (one row of 16384 slots: 23 us against 46; 512 of them: 99 against 148).
+template <bool MANY>
+struct EvictCfg {
+  static constexpr int THREADS = MANY ? 256 : 1024, OWN = MANY ? 32 : 16, BLOCKS = MANY ? 4 : 1;
+};
 // Keys that one warp searches alone.
 constexpr int kEvictShort = 256;
 
@@ -114,14 +119,16 @@ constexpr int kEvictShort = 256;
 // 1) * per), so ranks by slot are prefix sums over the threads.  The cut -- the
 // budget-th largest key -- is found two bits at a time by counting: three
 // thresholds per look, counts added up by redux and once through shared memory.
-// What bounds it is the number of instructions (16 looks of a block over 8192
-// keys: 49 us for 512 rows), so once at most 256 keys are left in the interval
-// the search goes on among those, in one warp and without barriers.  A look whose
+// What bounds it is the number of instructions (all 16 looks by the whole block
+// over 8192 keys: 49 us for 512 rows, 37 as it is), so once at most 256 keys are
+// left in the interval the search goes on among those, in one warp and without
+// barriers.  A look whose
 // count is the budget itself ends the search.
-template <bool STORED>
-__global__ void __launch_bounds__(kEvictThreads, 4) evict_select_kernel(const __grid_constant__ EvictParams p) {
+template <bool STORED, bool MANY>
+__global__ void __launch_bounds__(EvictCfg<MANY>::THREADS, EvictCfg<MANY>::BLOCKS) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kEvictOwn = EvictCfg<MANY>::OWN;
   extern __shared__ uint32_t evict_keys[];
-  __shared__ int scan[64], counts[2][3][kEvictThreads / 32], short_n;
+  __shared__ int scan[64], counts[2][3][EvictCfg<MANY>::THREADS / 32], short_n;
   __shared__ uint32_t short_keys[kEvictShort], short_cut;
   griddep_wait_and_release();
   const int row = blockIdx.x, g = row % p.KV, b = (row / p.KV) % p.B, layer = row / (p.KV * p.B);

@@ -20,6 +20,11 @@
 //  * Within a tile: S = Q K^T (M = 128 rows, N = 128 keys) and O += P V with P
 //    in TMEM, one softmax thread per row, lazy rescaling, P handed over in two
 //    halves: the same scheme and register split as flash_attention.cuh.
+//  * What bounds it: the DRAM for a few rows over long caches (8B decode step,
+//    32 x 8192 keys: 1.07 GB in 167 us, 6.4 TB/s; 8B batch of 16-node trees:
+//    0.69 GB in 120 us), the tensor core and the exponentials for many rows (8B
+//    prompt of 8192: 483 us, 1139 TFLOP/s; flash_attention.cuh, which need not
+//    leave a sum that fp32 weights can be divided by, 440 us beside it).
 //  * V rows behind the sequence are zeroed in shared memory before the product
 //    (their probability is 0, but 0 x NaN is NaN), so the cache may hold
 //    anything there.
@@ -248,7 +253,9 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
             if (!mbar_wait(&bars.empty[st], ph ^ 1u, wait_ns)) return false;
             mbar_arrive_expect_tx(&bars.full[st], C::KV_BYTES);
             for (int c = 0; c < C::CHUNKS; ++c)
-              if (rs.groups == 1)   // no other CTA reads this tile: the L2 is for records and scores
+              // No other CTA reads this tile: the L2 is for records and scores (8B decode
+              // step observed 203 -> 189 us, 8B batch of trees 127 -> 120).
+              if (rs.groups == 1)
                 tma_load_4d_once(smem + C::OFF_RING + st * C::KV_BYTES + c * C::TILE, is_v ? &mapV : &mapK,
                                  &bars.full[st], c * 64, g, (w0 + j) * 128, b, once);
               else

@@ -6,13 +6,13 @@
 // S^T = K Q^T with the 128 keys of a tile on the accumulator's lanes and 128
 // packed rows (position x head, as in rows_attention.cuh) on its columns.  A
 // thread owns one slot and adds up its columns in registers: no shuffle, no
-// atomic, one order for every run.  A segment is two key tiles, and two
-// threads per slot share its columns; the keys stay in shared memory while the query tiles stream past, each
-// read once for both (a single key tile per query tile would ask the L2 for 64
-// bytes per cycle and SM: 421 us against 332 us on the 8B prompt of 8192).
-// The bound is the exponential unit: 16 per cycle and SM, so a quarter of the
-// exponentials goes to the FMA pipe (the fine polynomial: the sums are fp32
-// results).
+// atomic, one order for every run.  A segment is two key tiles, and two threads
+// per slot share its columns; the keys stay in shared memory while the query
+// tiles stream past, each read once for both tiles (one key tile per query tile
+// asks the L2 for 64 bytes per cycle and SM: 421 us on the 8B prompt of 8192).
+// The bound is the exponentials: of 16 per cycle and SM a quarter goes to the FMA
+// pipe by the fine polynomial, since the sums are fp32 results (8B prompt: 327
+// us; with an eighth 340, three eighths 349, none 380).
 //
 // A few rows over a long cache (a decode step) leave their scores in the
 // workspace instead, and scored_weights_kernel below adds them up: K is then
