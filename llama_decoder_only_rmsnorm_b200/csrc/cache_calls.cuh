@@ -33,7 +33,14 @@ RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len)
   rs.tile_rows = p.tc ? 128 : kSimtTile;
   rs.qpt = std::max(1, rs.tile_rows / rs.rep);
   rs.tiles = (T + rs.qpt - 1) / rs.qpt;
-  p.pair = p.tc && rs.tiles > 1;
+  const long long keys = (long long)max_len + (tree ? 0 : T);
+  // Two row tiles per CTA share every K/V tile.  Out of little work, one row tile at
+  // a time makes longer runs of keys, and so fewer records to write and join: 28 us
+  // against 31 for a tree of 64 nodes over 8192 rows of the 8B heads, 20 against
+  // 22.5 over 2000, 49 alike over 30000.  Not for a chunk, which writes whole
+  // segments without records (8 x 517 rows: 51 us against 47).
+  const long long steps = (long long)B * rs.KV * rs.tiles * ((keys + 127) / 128);
+  p.pair = p.tc && rs.tiles > 1 && (!tree || steps > 16LL * num_sms());
   rs.slots = p.pair ? 2 : 1;
   rs.groups = (rs.tiles + rs.slots - 1) / rs.slots;
   rs.key_shift = p.tc ? 7 : 6;
@@ -42,7 +49,6 @@ RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len)
   // One CTA per SM for the tensor-core kernels, two of the others; no more than
   // there is work for.  (Four tiles at least per CTA, for fewer pieces to join:
   // 34 us against 27 for 4 sequences of 1000 fp32 keys.)
-  const long long keys = (long long)max_len + (tree ? 0 : T);
   const long long work = (long long)B * rs.groups * rs.KV * ((keys + (1 << rs.key_shift) - 1) >> rs.key_shift);
   rs.G = (int)std::min((long long)num_sms() * (p.tc ? 1 : 2), work);
   const long long units = (long long)B * rs.KV * rs.groups * (((keys + 63) >> rs.key_shift) + kFlatLead + 1);
