@@ -220,7 +220,7 @@ int run_observe(const llama3_config* c, RowsPlan& p, const ObserveArgs& a, cudaS
   w.cuts = rs.cuts;   // the attention's cuts have been joined when the weights' are written
   if (p.scored) {
     L3_LAUNCH(LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
-              launch_k(scored_weights_kernel, dim3((rs.max_len + rs.T + 1023) / 1024, rs.B * rs.KV), 256, 0, st, w));
+              launch_k(scored_weights_kernel, dim3((rs.max_len + rs.T - 1) / (256 * kScoredSlots) + 1, rs.B * rs.KV), 256, 0, st, w));
     return launch_check();
   }
   const long long most = (long long)w.B * w.key_tiles * w.KV * w.tiles;

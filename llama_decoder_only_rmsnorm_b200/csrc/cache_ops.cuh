@@ -348,9 +348,9 @@ __global__ void __launch_bounds__(256, 8) evict_move_kernel(const __grid_constan
     }
     const int fr = __ldg(ws + 4 + to);
     const size_t s = ((size_t)b * p.cap + fr) * slot16 + c, d = ((size_t)b * p.dst_cap + to) * slot16 + c;
-    const uint4 k = L.k[s], v = L.v[s];
-    L.dk[d] = k;
-    L.dv[d] = v;
+    const uint4 k = __ldcs(L.k + s), v = __ldcs(L.v + s);
+    __stcs(L.dk + d, k);
+    __stcs(L.dv + d, v);
     if (c == g * p.row16.d) {
       const size_t head = (size_t)b * p.KV + g;
       L.dw[head * p.dst_cap + to] = L.w[head * p.cap + fr];
