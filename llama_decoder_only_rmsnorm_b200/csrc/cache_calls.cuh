@@ -54,6 +54,10 @@ RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len)
   const long long units = (long long)B * rs.KV * rs.groups * (((keys + 63) >> rs.key_shift) + kFlatLead + 1);
   const long long sums = tree ? 0 : (long long)B * rs.KV * ((keys >> (p.tc ? 8 : 6)) + 1) * (rs.tiles + kFlatLead);
   p.fits = units < (1LL << 30) && sums < (1LL << 30);
+  // More than 64 pieces of a segment, if all segments are of one length, are joined by
+  // a launch of their own: 37 us against 61 with 148 pieces a row (one observed step
+  // over 60000 rows of one KV head of 128), 50 against 43 with 37 (four heads of 64).
+  rs.folded = rs.G / ((long long)B * rs.groups * rs.KV) > 64;
   const size_t records = tree ? (size_t)B * rs.groups * rs.KV + rs.G : (size_t)2 * rs.G;
   const size_t rows = records * rs.slots * rs.tile_rows;
   size_t off = 0;
@@ -143,7 +147,7 @@ int run_rows_simt_t(const RowsPlan& p, const void* q, const void* kc, const void
 
 // The main pass over the cache for T = float or bf16.
 template <typename T, int HD, bool TREE>
-int run_rows(const llama3_config* c, const RowsPlan& p, const void* q, const void* kc, const void* vc, int cap,
+int run_rows_main(const llama3_config* c, const RowsPlan& p, const void* q, const void* kc, const void* vc, int cap,
              cudaStream_t st) {
   if constexpr (std::is_same<T, bf16>::value && HD >= 32) {
     if (p.tc)
@@ -151,6 +155,17 @@ int run_rows(const llama3_config* c, const RowsPlan& p, const void* q, const voi
                     : run_rows_tc_t<HD, TREE, false>(c, p, q, kc, vc, cap, st);
   }
   return run_rows_simt_t<T, HD, TREE>(p, q, kc, vc, cap, st);
+}
+
+template <typename T, int HD, bool TREE>
+int run_rows(const llama3_config* c, const RowsPlan& p, const void* q, const void* kc, const void* vc, int cap,
+             cudaStream_t st) {
+  L3_TRY((run_rows_main<T, HD, TREE>(c, p, q, kc, vc, cap, st)));
+  if (!p.rs.folded) return LLAMA3_OK;
+  const int rows = std::min(p.rs.slots * p.rs.tile_rows, std::min(p.rs.T, p.rs.qpt * p.rs.slots) * p.rs.rep);
+  L3_LAUNCH(TREE ? LLAMA3_KERNEL_TREE_ATTENTION : LLAMA3_KERNEL_OBSERVED_ATTENTION, st,
+            launch_k((fold_pieces_kernel<HD, TREE>), dim3(p.rs.G - 1, rows), 32 * kFoldWarps, 0, st, p.rs));
+  return launch_check();
 }
 
 struct TreeArgs {

@@ -43,6 +43,7 @@ struct RowsShape {
   int slots, groups;                 // row tiles that a CTA works on together, and groups of them
   int key_shift;                     // log2 of a key tile (7 or 6)
   int G, max_len;                    // CTAs of the main kernel
+  int folded;                        // fold_pieces_kernel ran: a segment's first record stands for all
   float scale_log2;                  // log2(e) / sqrt(hd)
   const int32_t *kv_lens, *seq_lens;
   FlatCut* cuts;                     // [G] the plan, for the kernels that join
@@ -651,7 +652,13 @@ __device__ __forceinline__ void join_pieces(const RowsShape& rs, const FlatSeg& 
   for (int cb = c0; cb <= c1; cb += 32) {
     const int c = cb + lane;
     int w0 = 0, w1 = 0;
-    const bool some = c <= c1 && seg.cut(c * per, (c + 1) * per, w0, w1);
+    bool some = c <= c1 && seg.cut(c * per, (c + 1) * per, w0, w1);
+    if (rs.folded) {
+      const uint32_t any = __ballot_sync(0xffffffffu, some);
+      if (!any) continue;
+      some = lane == __ffs(any) - 1;
+      cb = c1;                 // and no further round
+    }
     const int id = some ? tiles_of.record(seg, c, c * per) : 0;
     uint32_t todo = __ballot_sync(0xffffffffu, some);
     float2 ml[NR];
@@ -704,6 +711,66 @@ __device__ __forceinline__ void join_pieces(const RowsShape& rs, const FlatSeg& 
       if (!todo) break;
       fetch();
     }
+  }
+}
+
+// Joins the pieces of segments that many CTAs share -- a long cache of few KV
+// heads -- into the record of the first, eight warps per row, so that the kernels
+// below have one record to read.  blockIdx.x + 1 is the CTA whose border is the
+// first within the segment, blockIdx.y a row of it.  What bounds it is the round
+// trips of a row's records: 148 pieces are five rounds for eight warps of four
+// pieces each, and 37 for one warp (an observed step over 60000 fp32 rows of two
+// KV heads of 16: 100 us in all against 131).
+constexpr int kFoldWarps = 8;
+template <int HD, bool TREE>
+__global__ void __launch_bounds__(32 * kFoldWarps) fold_pieces_kernel(const __grid_constant__ RowsShape rs) {
+  __shared__ float ms[kFoldWarps], ls[kFoldWarps], as[kFoldWarps][HD];
+  griddep_wait_and_release();
+  int per, b, grp, g;
+  const FlatSeg seg = flat_cut(rs.cuts, blockIdx.x + 1, per);
+  if (seg.n == 0) return;
+  const RowsTiles<TREE> tiles_of{rs};
+  tiles_of.where(seg, b, grp, g);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = rs.slots * rs.tile_rows;
+  const int c0 = seg.s0 / per, c1 = (seg.end() - 1) / per;
+  int w0, w1, first = c0;
+  while (!seg.cut(first * per, (first + 1) * per, w0, w1)) ++first;   // a segment has tiles, so it has a piece
+  if (w0 == 0 && w1 == seg.n) return;                                 // one piece
+  for (int r = blockIdx.y; r < R; r += gridDim.y) {
+    const int rt = grp * rs.slots + r / rs.tile_rows, t_in = r % rs.tile_rows / rs.rep;
+    if (t_in >= rs.qpt || rt * rs.qpt + t_in >= rs.T) continue;
+    RowAcc acc;
+    acc.clear();
+    for (int cb = first + warp; cb <= c1; cb += 4 * kFoldWarps) {     // four pieces in flight
+      float2 ml[4];
+      float4 o[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = cb + u * kFoldWarps;
+        ml[u] = make_float2(-INFINITY, 0.f);
+        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c > c1 || !seg.cut(c * per, (c + 1) * per, w0, w1)) continue;
+        const size_t id = tiles_of.record(seg, c, c * per);
+        ml[u] = *reinterpret_cast<const float2*>(rs.part_ml + (id * R + r) * 2);
+        if (lane < HD / 4) o[u] = load4(rs.part_o + ((id * (HD / 4) + lane) * R + r) * 4);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) acc.add(ml[u].x, ml[u].y, o[u]);
+    }
+    if (lane == 0) { ms[warp] = acc.m; ls[warp] = acc.l; }
+    if (lane < HD / 4) store4(&as[warp][4 * lane], acc.a[0], acc.a[1], acc.a[2], acc.a[3]);
+    __syncthreads();
+    if (warp == 0) {
+      acc.clear();
+#pragma unroll
+      for (int w = 0; w < kFoldWarps; ++w)
+        acc.add(ms[w], ls[w], lane < HD / 4 ? load4(&as[w][4 * lane]) : make_float4(0.f, 0.f, 0.f, 0.f));
+      const size_t id = tiles_of.record(seg, first, first * per);
+      if (lane == 0) *reinterpret_cast<float2*>(rs.part_ml + (id * R + r) * 2) = make_float2(acc.m, acc.l);
+      if (lane < HD / 4)
+        store4(rs.part_o + ((id * (HD / 4) + lane) * R + r) * 4, acc.a[0], acc.a[1], acc.a[2], acc.a[3]);
+    }
+    __syncthreads();
   }
 }
 
@@ -848,14 +915,16 @@ __global__ void __launch_bounds__(CausalJoin<HD>::THREADS) causal_join_kernel(co
   float m = -INFINITY, l = 0.f, a[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) a[i] = 0.f;
-  for (int c = c0; c <= c1; c += 2) {        // two pieces in flight
+  bool done = false;
+  for (int c = c0; c <= c1 && !done; c += 2) {        // two pieces in flight
     float2 ml[2];
     float4 o[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       int w0, w1;
       ml[u] = make_float2(-INFINITY, 0.f);
-      if (c + u > c1 || !seg.cut((c + u) * per, (c + u + 1) * per, w0, w1)) continue;
+      if (done || c + u > c1 || !seg.cut((c + u) * per, (c + u + 1) * per, w0, w1)) continue;
+      done = rs.folded;
       if (w0 == 0 && w1 == seg.n) return;    // whole: written by its CTA, no record
       const size_t id = tiles_of.record(seg, c + u, (c + u) * per);
       ml[u] = *reinterpret_cast<const float2*>(rs.part_ml + (id * R + r) * 2);

@@ -153,6 +153,16 @@ def test_tree_attention_long_cache_is_split():
     run_tree(2, 2, 64, "f32", [9001], 3, par[:, :3])
 
 
+@pytest.mark.parametrize("H,KV,hd,dtype", [(16, 1, 128, "bf16"), (4, 2, 64, "bf16"), (2, 1, 16, "f32"), (3, 1, 96, "bf16")])
+def test_one_long_cache_of_few_heads(H, KV, hd, dtype):
+    # dozens of pieces per row; a second, short sequence has none or one
+    par = np.stack([make_tree(np.random.default_rng(4), 6, "random", n) for n in (6, 3)])
+    for lens in ([12000], [15001, 100], [9000, 0]):
+        run_tree(H, KV, hd, dtype, lens, 6, par[:len(lens)])
+        run_observe(H, KV, hd, dtype, lens, 1, [1] * len(lens))
+        run_observe(H, KV, hd, dtype, lens, 5, [5, 2][:len(lens)])
+
+
 def test_tree_attention_plain_kernels_agree():
     par = make_tree(np.random.default_rng(2), 40, "random", 37)[None]
     run_tree(8, 2, 128, "bf16", [300], 40, par, path=1)
