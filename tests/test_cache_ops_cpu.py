@@ -2,6 +2,8 @@
 before anything is launched, and their oracle agrees with the causal oracle and
 with examples worked out by hand."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -203,3 +205,16 @@ def test_acceptance_oracle_by_hand():
     assert C.accept(draft, np.array([10, 13, 12, 77, 78, 79]), par) == ([0, 1, 5], 79)
     assert C.accept(draft, np.array([99, 13, 12, 77, 78, 79]), par) == ([0], 99)
     assert C.accept(draft, np.array([11, 13, 12, 77, 78, 79]), np.array([-2, 0, 0, 2, 2, 1])) == ([], -1)
+
+
+def test_fine_exponential_polynomial():
+    # the constants of exp2_poly2_fine, evaluated as the kernel does, against 2^f on [-1/2, 1/2]
+    src = open(os.path.join(os.path.dirname(B.__file__), "csrc", "rows_attention.cuh")).read()
+    body = src[src.index("void exp2_poly2_fine("):]
+    c = [np.float32(x) for x in re.findall(r"f2_pack\(([0-9.]+)f, ", body[:body.index("f2_unpack")])]
+    assert len(c) == 6                                   # degree 5, highest first
+    f = np.linspace(-0.5, 0.5, 100001).astype(np.float32)
+    p = np.full_like(f, c[0])
+    for k in c[1:]:
+        p = (p.astype(np.float64) * f + k).astype(np.float32)      # one rounding per fused step
+    assert np.abs(p / np.exp2(f.astype(np.float64)) - 1).max() < 2.4e-7
