@@ -37,6 +37,9 @@ struct FlatSeg {
   int item, sub, n;
   int s0;
   __device__ __forceinline__ int end() const { return s0 + n + kFlatLead; }
+  // The CTAs, of runs of `per` units, that work on its first and on its last tile.
+  __device__ __forceinline__ int first_cta(int per) const { return (s0 + kFlatLead) / per; }
+  __device__ __forceinline__ int last_cta(int per) const { return (end() - 1) / per; }
   // The tiles [w0, w1) of this segment within the units [a, e); false if there are none.
   __device__ __forceinline__ bool cut(int a, int e, int& w0, int& w1) const {
     w0 = max(0, a - s0 - kFlatLead);

@@ -679,17 +679,11 @@ __device__ __forceinline__ void join_pieces(const RowsShape& rs, const FlatSeg& 
   constexpr int U = NR == 4 ? 2 : 4;
   const RowsTiles<true> tiles_of{rs};
   const int lane = threadIdx.x & 31, R = rs.slots * rs.tile_rows;
-  const int c0 = seg.s0 / per, c1 = (seg.end() - 1) / per;
+  const int c0 = seg.first_cta(per), c1 = rs.folded ? c0 : seg.last_cta(per);
   for (int cb = c0; cb <= c1; cb += 32) {
     const int c = cb + lane;
     int w0 = 0, w1 = 0;
-    bool some = c <= c1 && seg.cut(c * per, (c + 1) * per, w0, w1);
-    if (rs.folded) {
-      const uint32_t any = __ballot_sync(0xffffffffu, some);
-      if (!any) continue;
-      some = lane == __ffs(any) - 1;
-      cb = c1;                 // and no further round
-    }
+    const bool some = c <= c1 && seg.cut(c * per, (c + 1) * per, w0, w1);
     const int id = some ? tiles_of.record(seg, c, c * per) : 0;
     uint32_t todo = __ballot_sync(0xffffffffu, some);
     float2 ml[NR];
@@ -763,10 +757,9 @@ __global__ void __launch_bounds__(32 * kFoldWarps) fold_pieces_kernel(const __gr
   const RowsTiles<TREE> tiles_of{rs};
   tiles_of.where(seg, b, grp, g);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = rs.slots * rs.tile_rows;
-  const int c0 = seg.s0 / per, c1 = (seg.end() - 1) / per;
-  int w0, w1, first = c0;
-  while (!seg.cut(first * per, (first + 1) * per, w0, w1)) ++first;   // a segment has tiles, so it has a piece
-  if (w0 == 0 && w1 == seg.n) return;                                 // one piece
+  const int first = seg.first_cta(per), c1 = seg.last_cta(per);
+  if (first == c1) return;     // one piece
+  int w0, w1;
   for (int r = blockIdx.y; r < R; r += gridDim.y) {
     const int rt = grp * rs.slots + r / rs.tile_rows, t_in = r % rs.tile_rows / rs.rep;
     if (t_in >= rs.qpt || rt * rs.qpt + t_in >= rs.T) continue;
@@ -942,21 +935,19 @@ __global__ void __launch_bounds__(CausalJoin<HD>::THREADS) causal_join_kernel(co
   const int rt = grp * rs.slots + r / rs.tile_rows, in = r % rs.tile_rows;
   const int t_in = in / rs.rep, t = rt * rs.qpt + t_in, h = g * rs.rep + in - t_in * rs.rep;
   if (t_in >= rs.qpt || t >= cached_len(rs.seq_lens, b, rs.T)) return;
-  const int c0 = seg.s0 / per, c1 = (seg.end() - 1) / per;
+  const int c0 = seg.first_cta(per), c1 = rs.folded ? c0 : seg.last_cta(per);
+  if (c0 == seg.last_cta(per)) return;       // whole: written by its CTA, no record
   float m = -INFINITY, l = 0.f, a[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) a[i] = 0.f;
-  bool done = false;
-  for (int c = c0; c <= c1 && !done; c += 2) {        // two pieces in flight
+  for (int c = c0; c <= c1; c += 2) {        // two pieces in flight
     float2 ml[2];
     float4 o[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       int w0, w1;
       ml[u] = make_float2(-INFINITY, 0.f);
-      if (done || c + u > c1 || !seg.cut((c + u) * per, (c + u + 1) * per, w0, w1)) continue;
-      done = rs.folded;
-      if (w0 == 0 && w1 == seg.n) return;    // whole: written by its CTA, no record
+      if (c + u > c1 || !seg.cut((c + u) * per, (c + u + 1) * per, w0, w1)) continue;
       const size_t id = tiles_of.record(seg, c + u, (c + u) * per);
       ml[u] = *reinterpret_cast<const float2*>(rs.part_ml + (id * R + r) * 2);
 #pragma unroll
