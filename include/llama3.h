@@ -379,7 +379,8 @@ int llama3_tree_workspace_size(const llama3_config* cfg, int batch, int n_nodes,
  *   out[b, t, h] = softmax_j(q[b,t,h] . k_j / sqrt(hd)) v_j
  * over the cached rows j = 0 .. kv_lens[b]-1 of (b, g) and, of the tree, the
  * node itself and its ancestors.  Other nodes and the cache behind kv_lens[b]
- * have no influence, whatever they hold (infinities and NaN included).
+ * have no influence, whatever they hold (infinities and NaN included); a NaN
+ * in the query or in a key that the row does see makes its output NaN.
  * q: [batch, n_nodes, H, hd] and k_nodes, v_nodes: [batch, n_nodes, KV, hd],
  * rotated to the node's position (the cached length plus its depth, where
  * nothing was evicted); caches as in llama3_layer_forward; kv_lens: device
@@ -483,6 +484,8 @@ int llama3_observe_workspace_size(const llama3_config* cfg, int batch, int seq, 
  * Cache rows behind kv_lens[b] + seq_lens[b] and padding rows of q have no
  * influence, whatever they hold.  The chunk's live rows are expected to be
  * finite: an infinity or a NaN in one may reach the outputs of rows before it.
+ * A NaN in a row's query or in a key that it sees makes its output NaN, and
+ * every weight that it hands out.
  * The sums have a fixed order: equal inputs give equal bits on one kind of GPU.
  * ws: llama3_observe_workspace_size(cfg, batch, seq, max_len) bytes; calls that
  * may run at the same time need workspaces of their own.

@@ -131,38 +131,68 @@ struct RowsCfg {
   static_assert(HD % 32 == 0 && HD <= 128, "head_dim");
 };
 
-// 2^x for two x <= 0 as exp2_poly2, with a polynomial of degree 5 (this
-// project's own fit, max relative error 2.4e-7): the accumulated weights and the
-// row sums that they are divided by are fp32 results.
-__device__ __forceinline__ void exp2_poly2_fine(float x0, float x1, float& y0, float& y1) {
-  const float shift = 12582912.0f;  // 1.5 * 2^23
-  const uint64_t x = f2_pack(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// max(x, floor), NaN where x is one (fmaxf gives the floor)
+__device__ __forceinline__ float max_or_nan(float x, float floor) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(floor));
+  return y;
+}
+
+// 2^x = p * 2^n for two x <= 0 by the range reduction of exp2_poly2, with a
+// polynomial of degree 5 (this project's own fit, max relative error 2.4e-7): the
+// accumulated weights and the row sums that they are divided by are fp32 results.
+// `shift` is 1.5 * 2^23 plus a small integer k, and t's low bits hold n + k.  Where
+// x is a NaN, p and t are the canonical one.
+__device__ __forceinline__ void exp2_poly2_fine(float shift, float x0, float x1, uint64_t& p, float& t0, float& t1) {
+  const uint64_t x = f2_pack(max_or_nan(x0, -126.0f), max_or_nan(x1, -126.0f));
   const uint64_t t = f2_add(x, f2_pack(shift, shift));
   const uint64_t f = f2_fma(f2_add(t, f2_pack(-shift, -shift)), f2_pack(-1.0f, -1.0f), x);
-  uint64_t p = f2_pack(0.001327647129073739f, 0.001327647129073739f);
+  p = f2_pack(0.001327647129073739f, 0.001327647129073739f);
   p = f2_fma(p, f, f2_pack(0.009675541892647743f, 0.009675541892647743f));
   p = f2_fma(p, f, f2_pack(0.05550713092088699f, 0.05550713092088699f));
   p = f2_fma(p, f, f2_pack(0.24022120237350464f, 0.24022120237350464f));
   p = f2_fma(p, f, f2_pack(0.6931469440460205f, 0.6931469440460205f));
   p = f2_fma(p, f, f2_pack(1.0000001192092896f, 1.0000001192092896f));
-  float p0, p1, t0, t1;
-  f2_unpack(p, p0, p1);
   f2_unpack(t, t0, t1);
+}
+// 2^x, NaN where x is one: 2^n is a factor, as adding n to the exponent of a NaN
+// makes a number of it.
+__device__ __forceinline__ void exp2_poly2_nan(float x0, float x1, float& y0, float& y1) {
+  uint64_t p;
+  float t0, t1;
+  exp2_poly2_fine(12583039.0f, x0, x1, p, t0, t1);   // k = 127: the low bits are the exponent field of 2^n
+  f2_unpack(f2_mul(p, f2_pack(__int_as_float(__float_as_int(t0) << 23), __int_as_float(__float_as_int(t1) << 23))), y0,
+            y1);
+}
+// 2^x, the largest finite number where x is a NaN (0x7fffffff plus the same moved up
+// by 23 bits): one instruction less per number.
+__device__ __forceinline__ void exp2_poly2_huge(float x0, float x1, float& y0, float& y1) {
+  uint64_t p;
+  float p0, p1, t0, t1;
+  exp2_poly2_fine(12582912.0f, x0, x1, p, t0, t1);
+  f2_unpack(p, p0, p1);
   y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
   y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
 
 // p = 2^(s * scl - m) for 32 scores in place and their sum; the FMA pipe takes
-// 4 of 16 pairs of an unmasked row, or, FINE, 2 with the fine polynomial (8B
-// prompt: 832 k cycles against 872 k with 4 and 839 k with none).
-template <bool MASKED, bool FINE>
+// 2 of 16 pairs of an unmasked row (8B prompt: 832 k cycles against 872 k with 4
+// and 839 k with none; trees of 128 nodes over 8 x 8000 rows of 64: 59 us, 58 with 4
+// pairs by the cubic, which has no place for a NaN, and over 4 x 8000 rows of 128:
+// 65.4 against 66.0).
+template <bool MASKED>
 __device__ __forceinline__ void rows_exp(uint32_t (&r)[32], float scl, float neg_m, float& sa, float& sb) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float x0, x1, p0, p1;
     fma2(x0, x1, __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), scl, scl, neg_m, neg_m);
-    if (!MASKED && (i & 7) < (FINE ? 1 : 2)) {
-      if (FINE) exp2_poly2_fine(x0, x1, p0, p1); else exp2_poly2(x0, x1, p0, p1);
+    if (!MASKED && (i & 7) < 1) {
+      exp2_poly2_nan(x0, x1, p0, p1);
     } else {
       p0 = ex2_approx(x0);
       p1 = ex2_approx(x1);
@@ -172,12 +202,12 @@ __device__ __forceinline__ void rows_exp(uint32_t (&r)[32], float scl, float neg
     r[2 * i + 1] = __float_as_uint(p1);
   }
 }
-template <bool MASKED, bool FINE>
+template <bool MASKED>
 __device__ __forceinline__ float rows_exp_half(uint32_t (&ra)[32], uint32_t (&rb)[32], float scl, float neg_m,
                                                uint32_t taddr) {
   float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-  rows_exp<MASKED, FINE>(ra, scl, neg_m, s0, s1);
-  rows_exp<MASKED, FINE>(rb, scl, neg_m, s2, s3);
+  rows_exp<MASKED>(ra, scl, neg_m, s0, s1);
+  rows_exp<MASKED>(rb, scl, neg_m, s2, s3);
   flash_pack_store(ra, taddr);
   flash_pack_store(rb, taddr + 16);
   return (s0 + s1) + (s2 + s3);
@@ -516,9 +546,9 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
         const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
         float la, lb;
         if (need_mask)
-          la = rows_exp_half<true, !TREE>(ra, rb, rs.scale_log2, neg_m, s_tmem);
+          la = rows_exp_half<true>(ra, rb, rs.scale_log2, neg_m, s_tmem);
         else
-          la = rows_exp_half<false, !TREE>(ra, rb, rs.scale_log2, neg_m, s_tmem);
+          la = rows_exp_half<false>(ra, rb, rs.scale_log2, neg_m, s_tmem);
         if (!PAIR && merged) {
           // the first P.V of this piece overwrites O: the other warpgroup has to have read the last piece's
           if (!mbar_wait_warp(&bars.merge[1], mph ^ 1u, wait_ns)) { ok = false; break; }
@@ -528,9 +558,9 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
         tc_fence_before();
         mbar_arrive(&bars.p_half[slot]);
         if (need_mask)
-          lb = rows_exp_half<true, !TREE>(rc, rd, rs.scale_log2, neg_m, s_tmem + 32);
+          lb = rows_exp_half<true>(rc, rd, rs.scale_log2, neg_m, s_tmem + 32);
         else
-          lb = rows_exp_half<false, !TREE>(rc, rd, rs.scale_log2, neg_m, s_tmem + 32);
+          lb = rows_exp_half<false>(rc, rd, rs.scale_log2, neg_m, s_tmem + 32);
         l += la + lb;
         tc_wait_st();
         tc_fence_before();
@@ -645,9 +675,10 @@ struct RowAcc {
     l = 0.f;
     a[0] = a[1] = a[2] = a[3] = 0.f;
   }
-  // adds a piece; one that saw no key has nothing in its O
+  // adds a piece; one that saw no key has nothing in its O, but one of keys that
+  // are all not a number has the maximum -inf as well, and a NaN for its sum
   __device__ __forceinline__ void add(float pm, float pl, const float4& o) {
-    if (pm == -INFINITY) return;
+    if (pm == -INFINITY && pl == pl) return;
     const float mn = fmaxf(m, pm);
     const float f = m == -INFINITY ? 0.f : exp2f(m - mn), fp = exp2f(pm - mn);
     l = l * f + pl * fp;
@@ -955,7 +986,7 @@ __global__ void __launch_bounds__(CausalJoin<HD>::THREADS) causal_join_kernel(co
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      if (ml[u].x == -INFINITY) continue;    // no such piece, or the row saw no key in it
+      if (ml[u].x == -INFINITY && ml[u].y == ml[u].y) continue;    // no such piece, or the row saw no key in it
       const float mn = fmaxf(m, ml[u].x);
       const float f = m == -INFINITY ? 0.f : exp2f(m - mn), fp = exp2f(ml[u].x - mn);
       l = l * f + ml[u].y * fp;

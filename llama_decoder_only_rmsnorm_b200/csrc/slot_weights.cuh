@@ -96,7 +96,7 @@ __device__ __forceinline__ void weight_add(uint32_t (&r)[32], const float* nlse,
     p[1] = ex2_approx(x[1]);
     if (!MASKED && i % 2 == 0) {
       // a quarter of the exponentials
-      exp2_poly2_fine(x[2], x[3], p[2], p[3]);
+      exp2_poly2_huge(x[2], x[3], p[2], p[3]);
     } else {
       p[2] = ex2_approx(x[2]);
       p[3] = ex2_approx(x[3]);
@@ -292,6 +292,10 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       if (!mbar_wait_warp(&meet[kt], pieces & 1u, wait_ns)) break;
       if (!half) {
         sum += right[(pieces & 1u) * 256];
+        // No slot receives more than a weight of 1 per row: beyond that lies what the
+        // polynomial makes of a row that is not a number (keeping its NaN there costs
+        // 20 us on the 8B prompt of 8192).
+        if (sum > 1e30f) sum = NAN;
         seg = box->seg;
         b = seg.item / ws.key_tiles;
         if (box->w0 == 0 && box->w1 == seg.n)
