@@ -428,8 +428,10 @@ int llama3_cache_evict(const llama3_config* cfg, const llama3_bounded_cache* src
   const bool many = (long long)std::min(n_layers, kEvictLayers) * batch * cfg->n_kv_heads >= 2LL * num_sms() &&
                     max_len <= EvictCfg<true>::THREADS * EvictCfg<true>::OWN;
   const bool stored = max_len <= kEvictKeys;
-  auto select = stored ? (many ? evict_select_kernel<true, true> : evict_select_kernel<true, false>)
-                       : (many ? evict_select_kernel<false, true> : evict_select_kernel<false, false>);
+  // many rows are stored ones: their slots fit the registers of 256 threads
+  static_assert(EvictCfg<true>::THREADS * EvictCfg<true>::OWN <= kEvictKeys, "eviction variants");
+  auto select = many ? evict_select_kernel<true, true>
+                     : stored ? evict_select_kernel<true, false> : evict_select_kernel<false, false>;
   // four slots per thread, up to the kernel's threads
   const int most_threads = many ? EvictCfg<true>::THREADS : EvictCfg<false>::THREADS;
   const int threads = std::max(64, std::min(most_threads, (int)(((long long)max_len / 4 + 31) / 32 * 32)));
