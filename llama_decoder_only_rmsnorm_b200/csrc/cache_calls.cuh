@@ -7,12 +7,12 @@ namespace {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// The tensor-core kernels take bf16 heads of 32 and more; fp32, head_dim 16 and
-// groups of more query heads than a tile has rows go to the CUDA cores.
+// The tensor-core kernels take bf16 heads of 32 and more, up to 128 query heads per
+// KV head; fp32, head_dim 16 and the plain kernel path go to the CUDA cores, which
+// take up to 64.  Larger groups are refused.
 bool rows_on_tc(const llama3_config* c) {
   return c->dtype == LLAMA3_DTYPE_BF16 && g_kernel_path != 1 && c->head_dim >= 32 && c->n_heads / c->n_kv_heads <= 128;
 }
-// Query rows of a tile on the CUDA cores; a KV head of more query heads than that is refused.
 bool rows_supported(const llama3_config* c) { return rows_on_tc(c) || c->n_heads / c->n_kv_heads <= kSimtTile; }
 
 // How T query positions per sequence over at most max_keys cached rows are laid
@@ -46,7 +46,8 @@ RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len)
   rs.key_shift = p.tc ? 7 : 6;
   rs.max_len = max_len;
   rs.scale_log2 = (float)(1.4426950408889634 / sqrt((double)c->head_dim));
-  // One CTA per SM for the tensor-core kernels, two of the others; no more than
+  // One CTA per SM for the tensor-core kernels, two of the others (of head_dim 128 an
+  // SM holds one at a time, 119 KB each, and takes the second after it); no more than
   // there is work for.  (Four tiles at least per CTA, for fewer pieces to join:
   // 34 us against 27 for 4 sequences of 1000 fp32 keys.)
   const long long work = (long long)B * rs.groups * rs.KV * ((keys + (1 << rs.key_shift) - 1) >> rs.key_shift);
@@ -55,8 +56,10 @@ RowsPlan plan_rows(const llama3_config* c, bool tree, int B, int T, int max_len)
   const long long sums = tree ? 0 : (long long)B * rs.KV * ((keys >> (p.tc ? 8 : 6)) + 1) * (rs.tiles + kFlatLead);
   p.fits = units < (1LL << 30) && sums < (1LL << 30);
   // More than 64 pieces of a segment, if all segments are of one length, are joined by
-  // a launch of their own: 37 us against 61 with 148 pieces a row (one observed step
+  // a launch of their own: 37 us against 60 with 148 pieces a row (one observed step
   // over 60000 rows of one KV head of 128), 50 against 43 with 37 (four heads of 64).
+  // One long sequence among short ones counts by the average, and may so be joined by
+  // one warp per row although it has as many pieces: the host does not know the lengths.
   rs.folded = rs.G / ((long long)B * rs.groups * rs.KV) > 64;
   const size_t records = tree ? (size_t)B * rs.groups * rs.KV + rs.G : (size_t)2 * rs.G;
   const size_t rows = records * rs.slots * rs.tile_rows;

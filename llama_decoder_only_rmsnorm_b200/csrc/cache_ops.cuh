@@ -102,12 +102,14 @@ __device__ __forceinline__ void block_scan2(int& x, int& y, int& tx, int& ty, in
 }
 
 // Order keys of a row that a block keeps in shared memory (128 KB); longer rows
-// compute them anew at every look.
+// compute them anew at every look, each thread along its own run of slots (16 rows
+// of 60000 slots, moves included: 286 us).
 constexpr int kEvictKeys = 32768;
 // Threads of a block at most, and the keys of each that stay in registers.  Many
 // rows: 256 threads of 32 keys, four blocks on an SM (512 rows are then one wave).
 // Fewer rows than two per SM, or more slots than that: 1024 threads of 16 keys
-// (one row of 16384 slots: 23 us against 46; 512 of them: 99 against 148).
+// (eviction in place to an eighth, moves included, of one row of 16384 slots: 30 us
+// against 49; of 512 of them with 128-wide heads: 314 against 380).
 template <bool MANY>
 struct EvictCfg {
   static constexpr int THREADS = MANY ? 256 : 1024, OWN = MANY ? 32 : 16, BLOCKS = MANY ? 4 : 1;

@@ -20,6 +20,10 @@
 //  * Within a tile: S = Q K^T (M = 128 rows, N = 128 keys) and O += P V with P
 //    in TMEM, one softmax thread per row, lazy rescaling, P handed over in two
 //    halves: the same scheme and register split as flash_attention.cuh.
+//  * The probabilities go to the tensor core in bf16, as its product with bf16 values
+//    wants them: each is off by 2^-8 at most, like the output's own rounding
+//    (relative error of the outputs against 64 bits 2.0e-3 to 2.3e-3; 1.7e-3 for fp32
+//    rounded once).  Their sum l takes them in fp32, before that rounding.
 //  * What bounds it: the DRAM for a few rows over long caches (8B decode step,
 //    32 x 8192 keys: 1.07 GB in 167 us, 6.4 TB/s; 8B batch of 16-node trees:
 //    0.69 GB in 120 us), the tensor core and the exponentials for many rows (8B
@@ -315,8 +319,9 @@ __global__ void __launch_bounds__(kFlashThreads, 1)
             if (!mbar_wait(&bars.empty[st], ph ^ 1u, wait_ns)) return false;
             mbar_arrive_expect_tx(&bars.full[st], C::KV_BYTES);
             for (int c = 0; c < C::CHUNKS; ++c)
-              // No other CTA reads this tile: the L2 is for records and scores (8B decode
-              // step observed 203 -> 189 us, 8B batch of trees 127 -> 120).
+              // No other CTA of this launch reads this tile: the L2 is for records and scores
+              // (8B decode step observed 203 -> 189 us, 8B batch of trees 127 -> 120).  Observed
+              // rows whose scores are not kept do read K again, in the launch of the weights.
               if (rs.groups == 1)
                 tma_load_4d_once(smem + C::OFF_RING + st * C::KV_BYTES + c * C::TILE, is_v ? &mapV : &mapK,
                                  &bars.full[st], c * 64, g, (w0 + j) * 128, b, once);

@@ -10,9 +10,13 @@
 // per slot share its columns; the keys stay in shared memory while the query
 // tiles stream past, each read once for both tiles (one key tile per query tile
 // asks the L2 for 64 bytes per cycle and SM: 421 us on the 8B prompt of 8192).
-// The bound is the exponentials: of 16 per cycle and SM a quarter goes to the FMA
-// pipe by the fine polynomial, since the sums are fp32 results (8B prompt: 327
-// us; with an eighth 340, three eighths 349, none 380).
+// Of the exponentials, 16 per cycle and SM, a quarter goes to the FMA pipe by the
+// fine polynomial, since the sums are fp32 results (8B prompt: 327 us; with an
+// eighth 340, three eighths 349, none 380).  No pipe is full: under the profiler
+// the exponentials' one is busy 57 % of the cycles, the tensor core 36 %, and 59 %
+// issue an instruction.  A thread waits for all of its 64 columns before the first
+// exponential, and 640 threads of 96 registers leave no room to hold two loads (24
+// bytes of the plan spill as it is).
 //
 // A few rows over a long cache (a decode step) leave their scores in the
 // workspace instead, and scored_weights_kernel below adds them up: K is then
