@@ -43,6 +43,13 @@ METRIC = "prefill & decode tokens/s on 1 B200; % of bf16 tensor / HBM roofline"
 PREFILL, DECODE = I.WORKLOADS["llama3_8b_prefill"], I.WORKLOADS["llama3_8b_decode"]
 PEAKS_PATH = os.path.join(ROOT, "MEASURED_PEAKS.json")
 TRAFFIC_PATH = os.path.join(ROOT, "profiles", "traffic.json")
+# sources that a recorded kernel's DRAM traffic stands for
+TRAFFIC_SOURCES = {
+    "gemm_w13": ["llama_decoder_only_rmsnorm_b200/csrc/tc_gemm.cuh",
+                 "llama_decoder_only_rmsnorm_b200/csrc/tc_gemm_pair.cuh",
+                 "llama_decoder_only_rmsnorm_b200/csrc/llama3.cu"],
+    "decode_attention": ["llama_decoder_only_rmsnorm_b200/csrc/decode_attention.cuh"],
+}
 # Used only when MEASURED_PEAKS.json is absent: the pool's earlier measurement
 # of a plain copy (HBM) and of a cuBLAS bf16 GEMM burst.  No sustained figure
 # exists for the fallback, so a kernel inside a long step is compared with the
@@ -105,7 +112,7 @@ def source_hash(files):
     return h.hexdigest()[:16]
 
 
-def recorded_traffic(kind, files):
+def recorded_traffic(kind):
     """Per-launch DRAM bytes from a committed ncu capture, if the kernel's
     sources are unchanged since it was taken; else None."""
     try:
@@ -113,7 +120,7 @@ def recorded_traffic(kind, files):
             rec = json.load(f).get(kind)
     except (OSError, ValueError):
         return None
-    if not rec or rec.get("source_sha") != source_hash(files):
+    if not rec or rec.get("source_sha") != source_hash(TRAFFIC_SOURCES[kind]):
         return None
     return rec.get("traffic_bytes_per_launch")
 
@@ -398,9 +405,7 @@ def run_ours(args):
     roofline = {"bound": "tensor", "kernel": "tc_gemm_pair w1|w3 + SwiGLU (M=8192, N=2x14336, K=4096; CTA pairs)",
                 "achieved": achieved, "peak": peak, "unit": "TFLOP/s",
                 "frac": (achieved / peak) if achieved else None, "peak_source": peak_src,
-                "traffic": recorded_traffic("gemm_w13", ["llama_decoder_only_rmsnorm_b200/csrc/tc_gemm.cuh",
-                                                         "llama_decoder_only_rmsnorm_b200/csrc/tc_gemm_pair.cuh",
-                                                         "llama_decoder_only_rmsnorm_b200/csrc/llama3.cu"]),
+                "traffic": recorded_traffic("gemm_w13"),
                 "kernel_ms": k_ms, "timed_launches": len(w13)}
     total_flop = n_layers * (2.0 * S * 6.979e9 / 32) + 2.0 * D * PREFILL.vocab  # linear layers + LM head row
     attn_flop = n_layers * PREFILL.n_heads * 2.0 * S * (S + 1) * PREFILL.head_dim
@@ -503,9 +508,7 @@ def run_ours(args):
                                                           f"{Bd} sequences per launch)",
                                "achieved": dach, "peak": hbm, "unit": "GB/s",
                                "frac": (dach / hbm) if dach else None, "peak_source": f"{peak_kind} hbm_gbs",
-                               "traffic": recorded_traffic("decode_attention", [
-                                   "llama_decoder_only_rmsnorm_b200/csrc/decode_attention.cuh"])
-                               if Bd == Bt else None,
+                               "traffic": recorded_traffic("decode_attention") if Bd == Bt else None,
                                "kernel_ms": dk_ms},
                   "decode_gemms": gemms,
                   "whole_step": {"bytes_per_step": step_bytes, "gbs": step_bytes / (dms / 1e3) / 1e9,
